@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define MHC_ABI_VERSION 5
+#define MHC_ABI_VERSION 6
 
 typedef enum mhc_dtype { MHC_F32 = 0, MHC_BF16 = 1 } mhc_dtype;
 
@@ -243,6 +243,169 @@ mhc_status mhc_post_stable_bwd(const mhc_desc* desc, const void* dx_next, const 
  * race and must not be made. */
 mhc_status mhc_pre_noalloc(const mhc_desc* desc, const void* x, const float* phi, const float* bias,
                            void* h, float* H_pre, float* H_post, float* H_res, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention sublayer an mHC block wraps: query/key norm with the rotary
+ * rotation, masked attention with its backward, and attention over a paged
+ * cache.
+ *
+ * Head tensors are [T][H][Dh] with the last two dimensions contiguous and a
+ * token stride of their own (`ld*`, in elements: a multiple of 8, at least
+ * H·Dh, at most 2^22), so that q, k and v may be views of one projection's
+ * output and their gradients views of its gradient.  Hq query heads share Hk
+ * key/value heads, Hq a multiple of Hk: query head h reads key head
+ * h / (Hq / Hk).  Everything else is contiguous.  The conventions of the top
+ * of this file hold (alignment, streams, errors, no allocation, no aliasing of
+ * outputs with inputs or one another, reproducible bits); arrays of indices
+ * and frequencies need their element's alignment only.  Device arrays of
+ * indices are read by the kernels and cannot be checked by the host: whatever
+ * they hold, no access leaves the tensors described here.
+ * ------------------------------------------------------------------------- */
+
+/* Shapes of the norm and rotation: R elements of each head are rotated (a
+ * multiple of 16, 16 ≤ R ≤ Dh), Dh a multiple of 16 up to 512; `interleaved`
+ * nonzero pairs elements (2i, 2i+1) of the rotated part, zero (i, i + R/2).
+ * ldv serves mhc_qk_rope_cache only; ldq_out and ldk_out are the strides of
+ * the outputs (of their gradients in the backward; ldk_out is not used by
+ * mhc_qk_rope_cache), ld_dq and ld_dk those of the backward's results. */
+typedef struct mhc_rope_desc {
+  int64_t T;
+  int32_t Hq;
+  int32_t Hk;
+  int32_t Dh;
+  int32_t R;
+  int32_t io;
+  int32_t interleaved;
+  float eps;
+  int32_t reserved; /* zero */
+  int64_t ldq, ldk, ldv;
+  int64_t ldq_out, ldk_out;
+  int64_t ld_dq, ld_dk;
+} mhc_rope_desc;
+
+/* Per head row x of q and of k, at the token's position p:
+ *   u = w ⊙ x · (mean_d x² + eps)^(-1/2)      (w = 1 if the weight is NULL)
+ *   each pair (a, b) of u's first R elements → (a cos θ - b sin θ, a sin θ + b cos θ),
+ *   θ = p·freqs[i], the others unchanged.
+ * positions[T] int32 (any value), freqs[R/2] double (radians per position;
+ * the angle is formed in 64 bits), q_weight[Dh], k_weight[Dh] fp32 or NULL. */
+mhc_status mhc_qk_rope(const mhc_rope_desc* desc, const void* q, const void* k, const int32_t* positions,
+                       const double* freqs, const float* q_weight, const float* k_weight, void* q_out, void* k_out,
+                       hipStream_t stream);
+
+/* Bytes of device workspace mhc_qk_rope_bwd needs; 0 for an invalid descriptor. */
+size_t mhc_qk_rope_bwd_workspace_bytes(const mhc_rope_desc* desc);
+
+/* Backward of mhc_qk_rope from q and k themselves: dq, dk, and the weights'
+ * gradients summed over tokens and heads, dq_weight[Dh] and dk_weight[Dh]
+ * (fp32, overwritten; each NULL to skip, and NULL where its weight is). */
+mhc_status mhc_qk_rope_bwd(const mhc_rope_desc* desc, const void* dq_out, const void* dk_out, const void* q,
+                           const void* k, const int32_t* positions, const double* freqs, const float* q_weight,
+                           const float* k_weight, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The serving form: q as by mhc_qk_rope; k normed and rotated, and v as it is,
+ * written to token place slots[t] of k_cache and v_cache [n_slots][Hk][Dh] (a
+ * paged cache [pages][page_size][Hk][Dh] has n_slots = pages·page_size; place
+ * = page·page_size + offset).  A token whose slot lies outside [0, n_slots)
+ * writes neither (padding: use -1); its q is computed all the same.  Two
+ * tokens must not share a slot (which one stays is then undefined). */
+mhc_status mhc_qk_rope_cache(const mhc_rope_desc* desc, const void* q, const void* k, const void* v,
+                             const int32_t* positions, const double* freqs, const float* q_weight,
+                             const float* k_weight, void* q_out, void* k_cache, void* v_cache, const int64_t* slots,
+                             int64_t n_slots, hipStream_t stream);
+
+/* Attention over packed documents.  docs (device, int32[n_docs + 1], sorted):
+ * document d is the rows docs[d] .. docs[d+1] - 1; NULL: one document of all T
+ * rows (n_docs is then ignored).  Row i sees the keys j of its own document;
+ * with causal nonzero those with j ≤ i, and of these
+ *   window > 0: only i - j < window;
+ *   prefix (device, int32[n_docs], or NULL): also every j among its document's
+ *     first prefix[d] rows.
+ * window and prefix need causal and exclude each other.  Scores:
+ *   s_ij = softcap·tanh(scale·q_i·k_j / softcap)  (scale·q_i·k_j if softcap is 0)
+ *          - slopes[h]·|i - j|                      (slopes: device fp32[Hq] or NULL)
+ * Rows of no document: with fill_outside nonzero their outputs are set to zero
+ * (lse to -inf), else they are left as they were; no row sees them as keys.
+ * Dh is 64 or 128; scale > 0, softcap ≥ 0.  ldo is the stride of o; ld_do,
+ * ld_dq, ld_dk, ld_dv serve the backward only. */
+typedef struct mhc_attn_desc {
+  int64_t T;
+  int32_t Hq;
+  int32_t Hk;
+  int32_t Dh;
+  int32_t io;
+  int32_t n_docs;
+  int32_t causal;
+  int32_t window;
+  int32_t fill_outside;
+  float scale;
+  float softcap;
+  const int32_t* docs;
+  const int32_t* prefix;
+  const float* slopes;
+  int64_t ldq, ldk, ldv, ldo;
+  int64_t ld_do, ld_dq, ld_dk, ld_dv;
+} mhc_attn_desc;
+
+/* o_i = Σ_j softmax_j(s_ij) v_j, and lse[Hq][T] (fp32, natural log; NULL to
+ * skip) for the backward. */
+mhc_status mhc_attn(const mhc_attn_desc* desc, const void* q, const void* k, const void* v, void* o, float* lse,
+                    hipStream_t stream);
+
+/* Bytes of device workspace mhc_attn_bwd needs; 0 for an invalid descriptor. */
+size_t mhc_attn_bwd_workspace_bytes(const mhc_attn_desc* desc);
+
+/* Backward of mhc_attn from its inputs, o and lse: dq[T][Hq][Dh], and dk, dv
+ * [T][Hk][Dh] summed over the query heads that share a key head.  slopes are
+ * constants.  Rows of no document as in the forward. */
+mhc_status mhc_attn_bwd(const mhc_attn_desc* desc, const void* dout, const void* q, const void* k, const void* v,
+                        const void* o, const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
+/* Attention of new tokens over a paged cache [num_pages][page_size][Hk][Dh].
+ * The rows of q and o are packed by sequence: sequence s has rows
+ * cu_q[s] .. cu_q[s+1] - 1 (device, int32[n_seqs + 1], sorted; NULL: row s
+ * alone), at most max_q of them (further rows are not computed).  kv_lens[s]
+ * (device, int32) counts its keys, the new tokens' included: the cache already
+ * holds those.  Key j lies in page pages[s][j / page_size] (device,
+ * int32[n_seqs][max_pages]) at offset j mod page_size; entries past the last
+ * key are not read, keys past max_pages·page_size do not exist.  Row c of
+ * q_len new ones is at position p = kv_len - q_len + c and sees the keys
+ * j ≤ p, of these with window > 0 only p - j < window, or else with prefix
+ * (device, int32[n_seqs]) also the keys j < prefix[s].  A row that sees no key
+ * gets zeros; a row whose sequence's keys lie in a page outside the cache gets
+ * NaN.  Rows of no sequence as rows of no document above.  Scores, Dh, strides
+ * as above; num_pages·page_size < 2^31. */
+typedef struct mhc_paged_desc {
+  int64_t T;
+  int32_t n_seqs;
+  int32_t max_q;
+  int32_t Hq;
+  int32_t Hk;
+  int32_t Dh;
+  int32_t io;
+  int32_t window;
+  int32_t page_size;
+  int32_t max_pages;
+  int32_t fill_outside;
+  int64_t num_pages;
+  float scale;
+  float softcap;
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* pages;
+  const int32_t* prefix;
+  const float* slopes;
+  int64_t ldq, ldo;
+} mhc_paged_desc;
+
+/* Bytes of device workspace mhc_attn_paged needs (0 if none, or for an invalid
+ * descriptor). */
+size_t mhc_attn_paged_workspace_bytes(const mhc_paged_desc* desc);
+
+mhc_status mhc_attn_paged(const mhc_paged_desc* desc, const void* q, const void* k_cache, const void* v_cache, void* o,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* MHC_ABI_VERSION of the built library. */
 int mhc_abi_version(void);

@@ -1,0 +1,442 @@
+// Device-side pieces shared by the attention kernels: matrix-core fragments,
+// LDS tiles and the rows' visible ranges.
+//
+// Every product runs on 32x32 accumulator blocks (v_mfma_f32_32x32x16_bf16, or
+// eight v_mfma_f32_32x32x2_f32 for fp32).  Lane l = 32·h + c:
+//   A operand: row c, B operand: column c, eight elements of the 16-wide inner
+//   axis each; the inner index is 8h + e for operands read along a row, and
+//   for operands formed from an accumulator 4h + e for e < 4, 8 + 4h + e - 4
+//   for the rest (any order serves as long as A and B agree);
+//   accumulator: column c, element r is row 8·(r/4) + 4h + r mod 4.
+// So a score block whose columns are the lane's own row of the softmax becomes
+// the B operand of the next product in the lane that holds it: the
+// probabilities never leave the registers.
+#pragma once
+
+#include "mhc_device.h"
+
+namespace mhc {
+namespace attn {
+
+constexpr int kThreads = 256;  // four waves
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+
+// Eight elements of an operand.
+template <int IO>
+struct Frag;
+template <>
+struct Frag<kBF16> {
+  u32x4_t w;
+};
+template <>
+struct Frag<kF32> {
+  float v[8];
+};
+
+__device__ __forceinline__ f32x16_t mma(const Frag<kBF16>& a, const Frag<kBF16>& b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a.w), __builtin_bit_cast(bf16x8_t, b.w),
+                                                 c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mma(const Frag<kF32>& a, const Frag<kF32>& b, f32x16_t c) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[e], b.v[e], c, 0, 0, 0);
+  return c;
+}
+
+// Eight consecutive elements of global memory (16-byte aligned).
+template <int IO>
+__device__ __forceinline__ Frag<IO> load_frag(const void* base, int64_t i) {
+  Frag<IO> f;
+  if constexpr (IO == kBF16)
+    f.w = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(base) + i);
+  else
+    load8<kF32>(base, i, f.v);
+  return f;
+}
+template <int IO>
+__device__ __forceinline__ Frag<IO> zero_frag() {
+  Frag<IO> f;
+  if constexpr (IO == kBF16) {
+    f.w = u32x4_t{0, 0, 0, 0};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = 0.f;
+  }
+  return f;
+}
+
+// The operand formed from accumulator elements 8·half .. 8·half + 7 of x.
+// bf16: each is rounded once, to the type the matrix cores take.
+template <int IO>
+__device__ __forceinline__ Frag<IO> frag_of(const f32x16_t& x, int half) {
+  Frag<IO> f;
+  if constexpr (IO == kBF16) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.w[e] = pack_bf16x2(x[8 * half + 2 * e], x[8 * half + 2 * e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = x[8 * half + e];
+  }
+  return f;
+}
+
+// A tile of head rows in LDS, 16-byte chunks.  Chunk c of row r lies at place
+// c ^ swz(r) of the row, so that the eight lanes of a 16-byte read of one
+// chunk in eight rows, and the four rows of a transposing read, fall on
+// different banks.
+template <int IO, int DH>
+struct Tile {
+  static constexpr int kElem = IoT<IO>::bytes;
+  static constexpr int kRow = DH * kElem;      // bytes of a row
+  static constexpr int kChunks = kRow / 16;    // 16-byte chunks of a row
+  static constexpr int kPer = 16 / kElem;      // elements of a chunk
+  __device__ static __forceinline__ int swz(int r) { return kChunks >= 16 ? (2 * r) & 15 : r & 6; }
+  __device__ static __forceinline__ int at(int r, int c) { return r * kRow + ((c ^ swz(r)) << 4); }
+
+  // Operand along the row: elements 16·s + 8·h + e of row r.
+  __device__ static __forceinline__ Frag<IO> row_frag(const char* t, int r, int s, int h) {
+    Frag<IO> f;
+    if constexpr (IO == kBF16) {
+      f.w = *reinterpret_cast<const u32x4_t*>(t + at(r, 2 * s + h));
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(t + at(r, 4 * s + 2 * h));
+      const float4 b = *reinterpret_cast<const float4*>(t + at(r, 4 * s + 2 * h + 1));
+      f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
+      f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
+    }
+    return f;
+  }
+
+  // Operand across the rows: column 32·blk + c of rows r0 + 4h + {0..3} and
+  // r0 + 8 + 4h + {0..3} (the order of operands formed from an accumulator).
+  // bf16: ds_read_b64_tr_b16, whose 16 lanes read a 4 x 16 block (lane i the
+  // four elements from column 4·(i mod 4) of row i/4) and get its columns.
+  __device__ static __forceinline__ Frag<IO> col_frag(const char* t, int r0, int blk, int lane) {
+    Frag<IO> f;
+    const int h = lane >> 5;
+    if constexpr (IO == kBF16) {
+      typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_t;
+      const int i = lane & 15;
+      const int r = r0 + 4 * h + (i >> 2);
+      const int col = 32 * blk + (lane & 16) + 4 * (i & 3);
+      const int off = at(r, col >> 3) + (col & 7) * 2;
+      // rows r and r + 8 have the same swizzle
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(t + off));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(t + off + 8 * kRow));
+      const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
+      f.w = u32x4_t{a.x, a.y, b.x, b.y};
+    } else {
+      const int col = 32 * blk + (lane & 31);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = r0 + 8 * (e >> 2) + 4 * h + (e & 3);
+        f.v[e] = *reinterpret_cast<const float*>(t + at(r, col >> 2) + (col & 3) * 4);
+      }
+    }
+    return f;
+  }
+};
+
+// Staging of R head rows by the workgroup: global memory to registers, then
+// registers to LDS, so that the next tile is on its way while this one is
+// used.  Thread i takes chunk i mod C of rows i/C, i/C + 256/C, ...
+template <int IO, int DH, int R>
+struct Stage {
+  using T = Tile<IO, DH>;
+  static constexpr int kN = R * T::kChunks / kThreads;  // chunks a thread
+  static constexpr int kStep = kThreads / T::kChunks;   // rows between a thread's chunks
+  static_assert(R * T::kChunks % kThreads == 0, "whole passes");
+  u32x4_t w[kN];
+
+  // Rows base + 0 .. base + rows - 1, `ld` elements apart; the buffer's own
+  // bounds check returns zeros for rows past the last.
+  __device__ __forceinline__ void load(const void* base, int64_t ld, int rows) {
+    rows = min(rows, R);
+    const int row_bytes = (int)(ld * T::kElem);
+    const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)row_bytes + T::kRow : 0u;
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+    const uint32_t v0 = (uint32_t)(threadIdx.x / T::kChunks) * (uint32_t)row_bytes + (threadIdx.x % T::kChunks) * 16u;
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+      w[n] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(v0 + (uint32_t)(n * kStep) * (uint32_t)row_bytes), 0, 0);
+  }
+  __device__ __forceinline__ void store(char* t) const {
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+      *reinterpret_cast<u32x4_t*>(t + T::at(threadIdx.x / T::kChunks + n * kStep, threadIdx.x % T::kChunks)) = w[n];
+  }
+};
+
+// Entries of the sorted docs[0..cnt) that are ≤ i, for a wave-uniform i: each
+// step probes 64 entries, one a lane.  (Unsorted entries give some number in
+// 0..cnt, so no access leaves the array.)
+__device__ __forceinline__ int count_le(const int32_t* docs, int cnt, int i) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int lo = 0, hi = cnt;
+  while (lo < hi) {
+    const int step = (hi - lo + kWave - 1) / kWave;
+    const int64_t e = (int64_t)lo + (int64_t)(lane + 1) * step - 1;
+    const bool le = e < hi && docs[e] <= i;
+    const int c = __popcll(__ballot(le));
+    const int64_t nlo = (int64_t)lo + (int64_t)c * step, nhi = nlo + step - 1;
+    lo = (int)(nlo < hi ? nlo : hi);
+    hi = (int)(nhi < hi ? nhi : hi);
+  }
+  return lo;
+}
+
+// Masks of one packed batch of documents (the dense calls).
+struct DocMask {
+  const int32_t* docs;    // [n_docs + 1] or null: one document of all T rows
+  const int32_t* prefix;  // [n_docs] or null
+  int n_docs, T, causal, window;
+
+  // First and last row + 1 of row i's document, and the end of its prefix;
+  // false if the row belongs to none.  `a`..`b`: bounds of count_le(i).
+  __device__ __forceinline__ bool doc(int i, int a, int b, int& s, int& e, int& p) const {
+    if (docs == nullptr) {
+      s = 0;
+      e = T;
+      p = prefix != nullptr ? clampi(prefix[0], 0, T) : 0;
+      return i < T;
+    }
+    while (a < b) {  // largest count c in [a, b] with docs[c - 1] <= i
+      const int m = (a + b + 1) >> 1;
+      if (docs[m - 1] <= i) a = m; else b = m - 1;
+    }
+    if (a < 1 || a > n_docs || i >= T) return false;
+    s = clampi(docs[a - 1], 0, T);
+    e = clampi(docs[a], 0, T);
+    p = prefix != nullptr ? (int)min((int64_t)e, (int64_t)s + clampi(prefix[a - 1], 0, T)) : s;
+    return i >= s && i < e;
+  }
+  __device__ static __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+  // Bounds of count_le for the rows i0..i1 (wave-uniform).
+  __device__ __forceinline__ void bounds(int i0, int i1, int& a, int& b) const {
+    a = b = 0;
+    if (docs == nullptr) return;
+    a = count_le(docs, n_docs + 1, i0);
+    b = count_le(docs, n_docs + 1, i1);
+    if (b < a) b = a;
+  }
+  // Keys [lo, hi) that row i sees (empty for a row of no document).
+  __device__ __forceinline__ bool keys(int i, int a, int b, int& lo, int& hi) const {
+    int s, e, p;
+    lo = hi = 0;
+    if (!doc(i, a, b, s, e, p)) return false;
+    lo = s;
+    hi = e;
+    if (causal) {
+      hi = max(i + 1, p);
+      if (window > 0) lo = max(s, i - window + 1);
+    }
+    return true;
+  }
+  // Rows [lo, hi) that see key j.
+  __device__ __forceinline__ bool rows(int j, int a, int b, int& lo, int& hi) const {
+    int s, e, p;
+    lo = hi = 0;
+    if (!doc(j, a, b, s, e, p)) return false;
+    lo = s;
+    hi = e;
+    if (causal) {
+      lo = j < p ? s : j;
+      if (window > 0) hi = (int)min((int64_t)e, (int64_t)j + window);
+    }
+    return true;
+  }
+};
+
+// Smallest lo and largest hi over the wave's lanes with lo < hi (lo = hi = 0
+// where there is none).
+__device__ __forceinline__ void wave_range(int lo, int hi, int& wlo, int& whi) {
+  wlo = lo < hi ? lo : 0x7fffffff;
+  whi = lo < hi ? hi : 0;
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) {
+    wlo = min(wlo, __shfl_xor(wlo, off, kWave));
+    whi = max(whi, __shfl_xor(whi, off, kWave));
+  }
+  wlo = __builtin_amdgcn_readfirstlane(wlo);
+  whi = __builtin_amdgcn_readfirstlane(whi);
+  if (whi == 0) wlo = 0;
+}
+
+// The other half's value: lane l and l ^ 32.
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, kWave); }
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// tanh by one exponential of -2|x|: exact at both ends.  For small |x| the
+// difference 1 - e would lose digits, so the odd series takes over there: its
+// first dropped term is 62/2835·x⁹, 2⁻²⁶ of x at |x| = 0.17.
+__device__ __forceinline__ float tanh_fast(float x) {
+  const float t = exp2_fast(-2.f * kLog2e * fabsf(x));
+  const float big = (1.f - t) * __builtin_amdgcn_rcpf(1.f + t);
+  const float x2 = x * x;
+  const float small = fabsf(x) * (1.f + x2 * (-1.f / 3.f + x2 * (2.f / 15.f + x2 * (-17.f / 315.f))));
+  return copysignf(fabsf(x) < 0.17f ? small : big, x);
+}
+
+// How scores are formed from the products q·k, in units of log 2 so that exp2
+// serves: capped (cap·tanh(scale·x/cap), cap > 0), lowered by slope·distance.
+struct ScoreMod {
+  float scale, cap;
+  // the factor on q·k: to log 2 units at once, or to the tanh's argument
+  __host__ __device__ __forceinline__ float pre() const { return cap > 0.f ? scale / cap : scale * kLog2e; }
+  __host__ __device__ __forceinline__ float post() const { return cap * kLog2e; }
+};
+
+// tanh of the capping.  fp32: tanh_fast.  bf16: 1 - 2/(1 + e^2x), whose
+// absolute error of 2⁻²³ moves a score by cap·2⁻²³, far below a rounding of
+// its probability to bf16.
+template <int IO>
+__device__ __forceinline__ float cap_tanh(float x) {
+  if constexpr (IO == kF32) return tanh_fast(x);
+  return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + exp2_fast(2.f * kLog2e * x));
+}
+
+// Accumulator element r's row within its 32-row block, for lane half h.
+__device__ __forceinline__ constexpr int acc_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
+
+// One accumulator block's worth of an output row: column block `blk` of the
+// lane's row, elements 8i + 4h + {0..3}, scaled.
+template <int IO>
+__device__ __forceinline__ void store_block(void* out, int64_t row, int blk, int h, const f32x16_t& x, float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t at = row + 32 * blk + 8 * i + 4 * h;
+    const float a = x[4 * i] * f, b = x[4 * i + 1] * f, c = x[4 * i + 2] * f, d = x[4 * i + 3] * f;
+    if constexpr (IO == kBF16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(a, b, c, d);
+  }
+}
+
+// State of the lane's softmax row over the keys seen so far: running maximum
+// (log 2 units), this half's share of the sum, and the unnormalised output.
+template <int DH>
+struct RowState {
+  float m, l;
+  f32x16_t o[DH / 32];
+  __device__ __forceinline__ void init() {
+    m = -__builtin_inff();
+    l = 0.f;
+#pragma unroll
+    for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[b][r] = 0.f;
+  }
+};
+
+// Takes KB blocks of 32 keys into the row state: scores by S^T = K·Q^T,
+// masked to the lane's keys [lo, hi) where `partial`, then O^T += V^T·P^T.
+// `key0`: index of the tile's first key; `pos`: the row's own index.
+// The maximum is let lag by up to 2⁶: a new maximum rescales the output only
+// when it would overflow that margin (p stays ≤ 64, exact in fp32 sums, and
+// bf16 keeps its relative precision at any scale).
+template <int IO, int DH, int KB, bool MOD>
+__device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH / 16], const char* tk, const char* tv,
+                                       int key0, int lo, int hi, bool partial, int pos, float slope2, ScoreMod mod) {
+  using T = Tile<IO, DH>;
+  const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h = lane >> 5;
+  f32x16_t s[KB];
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < DH / 16; ++i) s[b] = mma(T::row_frag(tk, 32 * b + c, i, h), qf[i], s[b]);
+  }
+  float pre = mod.pre();
+  if constexpr (MOD) {
+    const float d0 = (float)(pos - key0 - 4 * h);
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float x = s[b][r] * pre;
+        if (mod.cap > 0.f) x = mod.post() * cap_tanh<IO>(x);
+        s[b][r] = __builtin_fmaf(-slope2, fabsf(d0 - (float)(32 * b + 8 * (r >> 2) + (r & 3))), x);
+      }
+    pre = 1.f;
+  }
+  if (partial) {
+    const int l0 = lo - key0 - 4 * h, h0 = hi - key0 - 4 * h;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int k = 32 * b + 8 * (r >> 2) + (r & 3);
+        s[b][r] = k >= l0 && k < h0 ? s[b][r] : -__builtin_inff();
+      }
+  }
+  float mx = s[0][0];
+#pragma unroll
+  for (int b = 0; b < KB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][r]);
+  mx = fmaxf(mx, other_half(mx)) * pre;
+  constexpr float kLag = 6.f;
+  if (__any(mx > st.m + kLag)) {
+    const float m = fmaxf(st.m, mx);
+    const float f = m == -__builtin_inff() ? 1.f : exp2_fast(st.m - m);
+    st.m = m;
+    st.l *= f;
+#pragma unroll
+    for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) st.o[b][r] *= f;
+  }
+  const float base = st.m == -__builtin_inff() ? 0.f : st.m;
+  float sum = 0.f;
+#pragma unroll
+  for (int b = 0; b < KB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[b][r] = exp2_fast(__builtin_fmaf(s[b][r], pre, -base));
+      sum += s[b][r];
+    }
+  st.l += sum;
+#pragma unroll
+  for (int b = 0; b < KB; ++b)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const Frag<IO> p = frag_of<IO>(s[b], i);
+#pragma unroll
+      for (int d = 0; d < DH / 32; ++d)
+        st.o[d] = mma(T::col_frag(tv, 32 * b + 16 * i, d, lane), p, st.o[d]);
+    }
+}
+
+}  // namespace attn
+
+// Calls f(io, head size, modified scores) as integral constants for the
+// supported kinds.
+template <typename F>
+__host__ bool dispatch_attn(int io, int dh, bool mod, F&& f) {
+  return dispatch_io(io, [&](auto io_) {
+    auto with_dh = [&](auto dh_) {
+      if (mod)
+        f(io_, dh_, std::true_type{});
+      else
+        f(io_, dh_, std::false_type{});
+    };
+    if (dh == 64)
+      with_dh(std::integral_constant<int, 64>{});
+    else if (dh == 128)
+      with_dh(std::integral_constant<int, 128>{});
+  });
+}
+
+}  // namespace mhc

@@ -1,0 +1,158 @@
+// Masked attention over packed documents, forward.
+//
+// For query head h and row i of a packed batch of T tokens:
+//   s_ij = cap·tanh(scale·q_i·k_j / cap) - slope_h·|i - j|   (each part optional)
+//   o_i  = Σ_j p_ij v_j,  p_i = softmax of s_i over the keys j that row i sees,
+//   lse_i = log Σ_j exp s_ij.
+// Row i sees the keys of its own document, and with `causal` of those only
+// j ≤ i (and i - j < window), or j in the document's prefix.  All these masks
+// leave one run of keys [lo, hi) per row, so a tile of rows walks the union of
+// its rows' runs and masks only the key tiles that some row sees in part.
+//
+// A workgroup takes 128 rows of one query head, 32 a wave, and walks the keys
+// in tiles of 64, staged through registers into two LDS buffers (one barrier a
+// tile).  One pass, with a running maximum and sum per row.
+#include "attn_core.h"
+#include "mhc_internal.h"
+
+namespace mhc {
+
+using namespace attn;
+
+namespace {
+
+constexpr int kRows = 128, kKeys = 64;
+
+struct FwdArgs {
+  DocMask mask;
+  ScoreMod mod;
+  const void *q, *k, *v;
+  const float* slopes;
+  void* o;
+  float* lse;  // [Hq][T] or null
+  int Hq, Hk, fill;
+  int64_t ldq, ldk, ldv, ldo;
+};
+
+template <int IO, int DH, bool MOD>
+__global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel(FwdArgs a) {
+  using T = Tile<IO, DH>;
+  constexpr int kTile = kKeys * T::kRow;
+  extern __shared__ __attribute__((aligned(256))) char lds[];  // two buffers of a key and a value tile
+  __shared__ int range[8];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  // Tiles from the last (under a causal mask the longest) down; the heads of a
+  // tile vary fastest, key head first: consecutive workgroups go to the eight
+  // XCDs in turn, so with 8 key heads (or a divisor) each XCD's L2 holds one
+  // head's keys and values.
+  const int G = a.Hq / a.Hk;
+  const int nt = (a.mask.T + kRows - 1) / kRows;
+  const int tile = nt - 1 - (int)(blockIdx.x / a.Hq), x = blockIdx.x % a.Hq;
+  const int hk = x % a.Hk, hq = hk * G + x / a.Hk;
+  const int i0 = tile * kRows + wave * 32, i = i0 + c;
+
+  int ba, bb, lo, hi, wlo, whi;
+  a.mask.bounds(i0, i0 + 31, ba, bb);
+  const bool in_doc = a.mask.keys(i, ba, bb, lo, hi);
+  wave_range(lo, hi, wlo, whi);
+  if (lane == 0) {
+    range[wave] = whi > 0 ? wlo : 0x7fffffff;
+    range[4 + wave] = whi;
+  }
+  __syncthreads();
+  int blo = min(min(range[0], range[1]), min(range[2], range[3]));
+  const int bhi = max(max(range[4], range[5]), max(range[6], range[7]));
+  if (bhi == 0) blo = 0;
+  // rows of no document take no part: any key tile is whole for them
+  const bool live = in_doc && lo < hi;
+
+  Frag<IO> qf[DH / 16];
+#pragma unroll
+  for (int s = 0; s < DH / 16; ++s)
+    qf[s] = i < a.mask.T ? load_frag<IO>(a.q, i * a.ldq + (int64_t)hq * DH + 16 * s + 8 * h) : zero_frag<IO>();
+
+  const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
+  const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
+  Stage<IO, DH, kKeys> sk, sv;
+  const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hq] * kLog2e : 0.f;
+  RowState<DH> st;
+  st.init();
+  // (rows past bhi read as zeros: no row of the tile sees them)
+  sk.load(kb + blo * a.ldk * T::kElem, a.ldk, bhi - blo);
+  sv.load(vb + blo * a.ldv * T::kElem, a.ldv, bhi - blo);
+  int buf = 0;
+  for (int key0 = blo; key0 < bhi; key0 += kKeys, buf ^= 1) {
+    char* tk = lds + buf * 2 * kTile;
+    char* tv = tk + kTile;
+    sk.store(tk);
+    sv.store(tv);
+    const int next = key0 + kKeys;
+    if (next < bhi) {
+      sk.load(kb + next * a.ldk * T::kElem, a.ldk, bhi - next);
+      sv.load(vb + next * a.ldv * T::kElem, a.ldv, bhi - next);
+    }
+    __syncthreads();
+    if (key0 < whi && next > wlo) {
+      const bool partial = __any(live && (lo > key0 || hi < next));
+      attend<IO, DH, kKeys / 32, MOD>(st, qf, tk, tv, key0, lo, hi, partial, i, slope2, a.mod);
+    }
+  }
+  if (i >= a.mask.T || (!in_doc && !a.fill)) return;
+  const float l = st.l + other_half(st.l);
+  const float inv = !live || l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int b = 0; b < DH / 32; ++b) {
+    if (!live)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) st.o[b][r] = 0.f;
+    store_block<IO>(a.o, i * a.ldo + (int64_t)hq * DH, b, h, st.o[b], inv);
+  }
+  if (a.lse != nullptr && h == 0)
+    a.lse[(int64_t)hq * a.mask.T + i] = live ? (st.m + __log2f(l)) * kLn2 : -__builtin_inff();
+}
+
+}  // namespace
+
+attn::DocMask doc_mask(const mhc_attn_desc& d) {
+  attn::DocMask m;
+  m.docs = d.docs;
+  m.prefix = d.prefix;
+  m.n_docs = d.docs != nullptr ? d.n_docs : 1;
+  m.T = (int)d.T;
+  m.causal = d.causal;
+  m.window = d.window;
+  return m;
+}
+
+hipError_t launch_attn(const mhc_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
+                       hipStream_t s) {
+  FwdArgs a{};
+  a.mask = doc_mask(d);
+  a.mod = {d.scale, d.softcap};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.slopes = d.slopes;
+  a.o = o;
+  a.lse = lse;
+  a.Hq = d.Hq;
+  a.Hk = d.Hk;
+  a.fill = d.fill_outside;
+  a.ldq = d.ldq;
+  a.ldk = d.ldk;
+  a.ldv = d.ldv;
+  a.ldo = d.ldo;
+  const dim3 grid((unsigned)((d.T + kRows - 1) / kRows * d.Hq));
+  hipError_t err = hipErrorInvalidValue;
+  dispatch_attn(d.io, d.Dh, d.softcap > 0.f || d.slopes != nullptr, [&](auto io_, auto dh_, auto mod_) {
+    constexpr int IO = decltype(io_)::value;
+    constexpr int DH = decltype(dh_)::value;
+    constexpr bool MOD = decltype(mod_)::value;
+    constexpr int lds = 4 * kKeys * Tile<IO, DH>::kRow;
+    MHC_LAUNCH((attn_fwd_kernel<IO, DH, MOD>), grid, dim3(kThreads), lds, s, a);
+    err = hipGetLastError();
+  });
+  return err;
+}
+
+}  // namespace mhc

@@ -1,0 +1,476 @@
+// Attention of new tokens over a paged cache: single tokens or a chunk per
+// sequence, keys and values read through each sequence's page table.
+//
+// Row t of sequence n is its q_len new tokens' c-th, at position
+// p = kv_len - q_len + c; it sees the keys j ≤ p (and p - j < window), or
+// j < prefix, of its sequence.  Scores as in the dense calls.
+//
+// The query heads that share a key head are packed into one tile of rows
+// (row = c·G + g), so that the cache is read once for all of them.  Two
+// kernels: up to 32 packed rows (single tokens, short drafts) go to four waves
+// that take different keys, each with LDS of its own and no barrier in the
+// loop; more rows go to the dense kernel's shape (128 rows, 32 a wave, over
+// shared key tiles of 64).  Where there are few rows the keys are split over
+// workgroups too; every split leaves a normalised partial row and its
+// log-sum-exp, and a second kernel joins them.
+//
+// Table entries outside the cache are never followed: the rows whose keys they
+// hold come out as NaN.
+#include "attn_core.h"
+#include "mhc_internal.h"
+
+namespace mhc {
+
+using namespace attn;
+
+namespace {
+
+constexpr int kFewRows = 32, kFewKeys = 32;
+constexpr int kRows = 128, kKeys = 64;
+constexpr int kMaxSplits = 64;
+
+// Division of 0 ≤ n < 2³¹ by a fixed d: with 2^(l-1) < d ≤ 2^l and
+// mul = ⌈2^(31+l)/d⌉, n·mul/2^(31+l) exceeds n/d by less than 1/d.
+struct Div {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int operator()(int n) const {
+    return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift);
+  }
+};
+Div div_of(uint32_t d) {
+  Div v{d, 0, 0};
+  if (d < 2) return v;
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  v.mul = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+  v.shift = l - 1;
+  return v;
+}
+
+struct PagedArgs {
+  int64_t T;
+  int n, max_q, Hq, Hk, window, max_pages, num_pages, page_size, fill, splits, tiles;
+  Div by_page, by_group;
+  ScoreMod mod;
+  const int32_t *cu, *prefix, *kv, *pages;
+  const float* slopes;
+  const void *q, *kc, *vc;
+  void* o;
+  float *part_o, *part_l;  // [splits][T][Hq][Dh], [splits][T][Hq]
+  int64_t ldq, ldo;
+};
+
+// Sequence `s`: its first row, number of rows and number of keys, all within
+// the tensors whatever the device arrays hold.
+struct Seq {
+  int64_t t0;
+  int nq, nk;
+  int before;  // keys before the first new token's own (negative: rows without keys)
+};
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+__device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s) {
+  Seq q;
+  int64_t t1;
+  if (a.cu == nullptr) {
+    q.t0 = s;
+    t1 = s + 1;
+  } else {
+    q.t0 = clamp64(a.cu[s], 0, a.T);
+    t1 = clamp64(a.cu[s + 1], q.t0, a.T);
+  }
+  q.nq = (int)(t1 - q.t0 < a.max_q ? t1 - q.t0 : a.max_q);
+  q.nk = (int)clamp64(a.kv[s], 0, (int64_t)a.max_pages * a.page_size);
+  q.before = (int)clamp64(q.nk - (t1 - q.t0), -(int64_t)0x7fffffff, q.nk);
+  return q;
+}
+
+// The packed row's token, head and keys.
+struct Row {
+  bool real;
+  int64_t at;   // (token, query head) as an index of [T][Hq]
+  int64_t tok;
+  int hq, pos, lo, hi;
+};
+__device__ __forceinline__ Row row_of(const PagedArgs& a, int s, const Seq& q, int hk, int pr) {
+  const int G = a.Hq / a.Hk;
+  Row r;
+  const int c = a.by_group(pr), g = pr - c * G;
+  r.real = c < q.nq;
+  r.tok = q.t0 + c;
+  r.hq = hk * G + g;
+  r.at = r.tok * a.Hq + r.hq;
+  r.pos = q.before + c;
+  r.lo = 0;
+  r.hi = min(q.nk, max(r.pos + 1, a.prefix != nullptr ? a.prefix[s] : 0));
+  if (a.window > 0) r.lo = max(0, r.pos - a.window + 1);
+  if (!r.real || r.hi <= r.lo) r.lo = r.hi = 0;
+  return r;
+}
+
+// Staging of R cache rows by NT threads: as Stage, with each row's place
+// looked up in the page table one tile ahead of its load.  Rows past `last`
+// re-read it (they are masked, and what is read is finite wherever the last
+// row's keys and values are).
+template <int IO, int DH, int R, int NT>
+struct PagedStage {
+  using T = Tile<IO, DH>;
+  static constexpr int kN = R * T::kChunks / NT;
+  static constexpr int kStep = NT / T::kChunks;
+  static_assert(R * T::kChunks % NT == 0 && NT % T::kChunks == 0, "whole passes");
+  u32x4_t k[kN], v[kN];
+  int place[kN];
+
+  __device__ __forceinline__ void lookup(const PagedArgs& a, const int32_t* table, int thread, int row0, int last,
+                                         bool& bad) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int r = min(row0 + thread / T::kChunks + n * kStep, last);
+      const int p = a.by_page(r);
+      int e = table[p];
+      if ((unsigned)e >= (unsigned)a.num_pages) {
+        bad = true;
+        e = 0;
+      }
+      place[n] = e * a.page_size + (r - p * a.page_size);
+    }
+  }
+  __device__ __forceinline__ void load(const PagedArgs& a, int hk, int thread) {
+    const int64_t row = (int64_t)a.Hk * T::kRow;
+    const int64_t in = (int64_t)hk * T::kRow + (thread % T::kChunks) * 16;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) k[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.kc) + place[n] * row + in);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) v[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.vc) + place[n] * row + in);
+  }
+  __device__ __forceinline__ void store(char* tk, char* tv, int thread) const {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int at = T::at(thread / T::kChunks + n * kStep, thread % T::kChunks);
+      *reinterpret_cast<u32x4_t*>(tk + at) = k[n];
+      *reinterpret_cast<u32x4_t*>(tv + at) = v[n];
+    }
+  }
+};
+
+// Rows that belong to no sequence, zeroed where the call asks for it.
+template <int IO, int DH>
+__device__ __forceinline__ void fill_rest(const PagedArgs& a) {
+  if (!a.fill) return;
+  const int64_t first = a.cu != nullptr ? clamp64(a.cu[0], 0, a.T) : 0;
+  const int64_t end = a.cu != nullptr ? clamp64(a.cu[a.n], 0, a.T) : a.n;
+  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (t >= first && t < end) continue;
+    for (int e = threadIdx.x * 8; e < a.Hq * DH; e += blockDim.x * 8) store8<IO>(a.o, t * a.ldo + e, z);
+  }
+}
+
+// Writes a finished row (or a split's share of it).
+template <int IO, int DH>
+__device__ __forceinline__ void finish(const PagedArgs& a, const Row& r, int sp, int h, RowState<DH>& st, float l, bool bad) {
+  float inv = l == 0.f ? 0.f : 1.f / l;
+  if (bad) inv = __builtin_nanf("");
+  if (a.splits == 1) {
+#pragma unroll
+    for (int b = 0; b < DH / 32; ++b) store_block<IO>(a.o, r.tok * a.ldo + (int64_t)r.hq * DH, b, h, st.o[b], inv);
+  } else {
+    const int64_t at = (int64_t)sp * a.T * a.Hq + r.at;
+#pragma unroll
+    for (int b = 0; b < DH / 32; ++b) store_block<kF32>(a.part_o, at * DH, b, h, st.o[b], inv);
+    if (h == 0) a.part_l[at] = bad ? __builtin_nanf("") : l == 0.f ? -__builtin_inff() : st.m + __log2f(l);
+  }
+}
+
+// Query fragments of a packed row.
+template <int IO, int DH>
+__device__ __forceinline__ void load_q(const PagedArgs& a, const Row& r, int h, Frag<IO> (&qf)[DH / 16]) {
+#pragma unroll
+  for (int s = 0; s < DH / 16; ++s)
+    qf[s] = r.real ? load_frag<IO>(a.q, r.tok * a.ldq + (int64_t)r.hq * DH + 16 * s + 8 * h) : zero_frag<IO>();
+}
+
+// The keys [lo, hi) of this split, whole tiles of `step` from the row tile's
+// first key on.
+__device__ __forceinline__ void split_range(int splits, int sp, int step, int& lo, int& hi) {
+  const int tiles = (hi - lo + step - 1) / step, per = (tiles + splits - 1) / splits;
+  const int64_t a = (int64_t)lo + (int64_t)sp * per * step, b = a + (int64_t)per * step;
+  lo = (int)(a < hi ? a : hi);
+  hi = (int)(b < hi ? b : hi);
+}
+
+// Few rows: one tile of up to 32 packed rows, which every wave holds; the
+// waves take the key tiles of 32 in turn and join their row states in LDS.
+template <int IO, int DH, bool MOD>
+__global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_kernel(PagedArgs a) {
+  using T = Tile<IO, DH>;
+  constexpr int kTile = kFewKeys * T::kRow;
+  extern __shared__ __attribute__((aligned(256))) char lds[];  // a key and a value tile a wave; then the waves' row states
+  __shared__ float wm[4][32], wl[4][32];
+  __shared__ int any_bad;
+  fill_rest<IO, DH>(a);
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  if (threadIdx.x == 0) any_bad = 0;
+  __syncthreads();
+  const int hk = blockIdx.x % a.Hk;
+  const int rest = blockIdx.x / a.Hk, sp = rest % a.splits, s = rest / a.splits;
+  const Seq q = seq_of(a, s);
+  if (q.nq == 0) return;
+  const Row r = row_of(a, s, q, hk, c);
+  int lo, hi;
+  wave_range(r.lo, r.hi, lo, hi);
+  split_range(a.splits, sp, kFewKeys, lo, hi);
+
+  Frag<IO> qf[DH / 16];
+  load_q<IO, DH>(a, r, h, qf);
+  const float slope2 = MOD && a.slopes != nullptr ? a.slopes[r.hq] * kLog2e : 0.f;
+  RowState<DH> st;
+  st.init();
+  bool bad = false;
+  char* tk = lds + wave * 2 * kTile;
+  char* tv = tk + kTile;
+  PagedStage<IO, DH, kFewKeys, kWave> sg;
+  const int32_t* table = a.pages + (int64_t)s * a.max_pages;
+  int key0 = lo + wave * kFewKeys;
+  constexpr int kAll = 4 * kFewKeys;
+  if (key0 < hi) {
+    sg.lookup(a, table, lane, key0, hi - 1, bad);
+    sg.load(a, hk, lane);
+    if (key0 + kAll < hi) sg.lookup(a, table, lane, key0 + kAll, hi - 1, bad);
+  }
+  for (; key0 < hi; key0 += kAll) {
+    sg.store(tk, tv, lane);
+    if (key0 + kAll < hi) sg.load(a, hk, lane);
+    if (key0 + 2 * kAll < hi) sg.lookup(a, table, lane, key0 + 2 * kAll, hi - 1, bad);
+    // the wave's own LDS: its writes come before its reads
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const bool partial = __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kFewKeys)) || key0 + kFewKeys > hi;
+    attend<IO, DH, 1, MOD>(st, qf, tk, tv, key0, r.lo, min(r.hi, hi), partial, r.pos, slope2, a.mod);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  if (__any(bad) && lane == 0) any_bad = 1;
+  if (r.lo >= r.hi) st.init();  // (unmasked tiles were not for this row)
+  // join the four waves' states
+  float l = st.l + other_half(st.l);
+  if (h == 0) {
+    wm[wave][c] = st.m;
+    wl[wave][c] = l;
+  }
+  __syncthreads();
+  float m = fmaxf(fmaxf(wm[0][c], wm[1][c]), fmaxf(wm[2][c], wm[3][c]));
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) l += wl[w][c] * exp2_fast(wm[w][c] - base);
+  const float f = exp2_fast(st.m - base);
+  // [wave][column block][element][lane]: each wave adds up one column block
+  float* acc = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[((wave * (DH / 32) + b) * 16 + e) * kWave + lane] = st.o[b][e] * f;
+  __syncthreads();
+  if (wave >= DH / 32 || !r.real) return;
+  f32x16_t sum;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) t += acc[((w * (DH / 32) + wave) * 16 + e) * kWave + lane];
+    sum[e] = t;
+  }
+  float inv = l == 0.f ? 0.f : 1.f / l;
+  if (any_bad) inv = __builtin_nanf("");
+  if (a.splits == 1) {
+    store_block<IO>(a.o, r.tok * a.ldo + (int64_t)r.hq * DH, wave, h, sum, inv);
+  } else {
+    const int64_t at = (int64_t)sp * a.T * a.Hq + r.at;
+    store_block<kF32>(a.part_o, at * DH, wave, h, sum, inv);
+    if (wave == 0 && h == 0) a.part_l[at] = any_bad ? __builtin_nanf("") : l == 0.f ? -__builtin_inff() : m + __log2f(l);
+  }
+}
+
+// Many rows: 128 packed rows of one sequence and key head, 32 a wave.
+template <int IO, int DH, bool MOD>
+__global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chunk_kernel(PagedArgs a) {
+  using T = Tile<IO, DH>;
+  constexpr int kTile = kKeys * T::kRow;
+  extern __shared__ __attribute__((aligned(256))) char lds[];
+  __shared__ int range[8];
+  __shared__ int any_bad;
+  fill_rest<IO, DH>(a);
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  const int hk = blockIdx.x % a.Hk;
+  int rest = blockIdx.x / a.Hk;
+  const int sp = rest % a.splits;
+  rest /= a.splits;
+  const int s = rest % a.n, tile = a.tiles - 1 - rest / a.n;
+  const int G = a.Hq / a.Hk;
+  const Seq q = seq_of(a, s);
+  if ((int64_t)tile * kRows >= (int64_t)q.nq * G) return;
+  const Row r = row_of(a, s, q, hk, tile * kRows + wave * 32 + c);
+  int wlo, whi;
+  wave_range(r.lo, r.hi, wlo, whi);
+  if (lane == 0) {
+    range[wave] = whi > 0 ? wlo : 0x7fffffff;
+    range[4 + wave] = whi;
+  }
+  if (threadIdx.x == 0) any_bad = 0;
+  __syncthreads();
+  int blo = min(min(range[0], range[1]), min(range[2], range[3]));
+  int bhi = max(max(range[4], range[5]), max(range[6], range[7]));
+  if (bhi == 0) blo = 0;
+  split_range(a.splits, sp, kKeys, blo, bhi);
+
+  Frag<IO> qf[DH / 16];
+  load_q<IO, DH>(a, r, h, qf);
+  const float slope2 = MOD && a.slopes != nullptr ? a.slopes[r.hq] * kLog2e : 0.f;
+  RowState<DH> st;
+  st.init();
+  bool bad = false;
+  PagedStage<IO, DH, kKeys, kThreads> sg;
+  const int32_t* table = a.pages + (int64_t)s * a.max_pages;
+  if (blo < bhi) {
+    sg.lookup(a, table, threadIdx.x, blo, bhi - 1, bad);
+    sg.load(a, hk, threadIdx.x);
+    if (blo + kKeys < bhi) sg.lookup(a, table, threadIdx.x, blo + kKeys, bhi - 1, bad);
+  }
+  int buf = 0;
+  for (int key0 = blo; key0 < bhi; key0 += kKeys, buf ^= 1) {
+    char* tk = lds + buf * 2 * kTile;
+    char* tv = tk + kTile;
+    sg.store(tk, tv, threadIdx.x);
+    if (key0 + kKeys < bhi) sg.load(a, hk, threadIdx.x);
+    if (key0 + 2 * kKeys < bhi) sg.lookup(a, table, threadIdx.x, key0 + 2 * kKeys, bhi - 1, bad);
+    __syncthreads();
+    if (key0 < whi && key0 + kKeys > wlo) {
+      const bool partial = __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kKeys)) || key0 + kKeys > bhi;
+      attend<IO, DH, kKeys / 32, MOD>(st, qf, tk, tv, key0, r.lo, min(r.hi, bhi), partial, r.pos, slope2, a.mod);
+    }
+  }
+  if (__any(bad) && lane == 0) any_bad = 1;
+  __syncthreads();
+  if (!r.real) return;
+  if (r.lo >= r.hi) st.init();  // (unmasked tiles were not for this row)
+  finish<IO, DH>(a, r, sp, h, st, st.l + other_half(st.l), any_bad != 0);
+}
+
+// Joins the splits' partial rows: one wave a row of [sequence][c][head].
+template <int IO, int DH>
+__global__ __launch_bounds__(kThreads) void attn_paged_join_kernel(PagedArgs a) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t n = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
+  const int64_t sc = n / a.Hq;
+  const int s = (int)(sc / a.max_q), c = (int)(sc % a.max_q), hq = (int)(n % a.Hq);
+  if (s >= a.n) return;
+  const Seq q = seq_of(a, s);
+  if (c >= q.nq) return;
+  const int64_t row = (q.t0 + c) * a.Hq + hq, all = a.T * a.Hq;
+  const float mine = lane < a.splits ? a.part_l[lane * all + row] : -__builtin_inff();
+  float m = mine;
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+  const float w = exp2_fast(mine - (m == -__builtin_inff() ? 0.f : m));
+  const float total = wave_sum(w);
+  constexpr int kPer = DH / kWave;
+  float acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  for (int i = 0; i < a.splits; ++i) {
+    const float wi = __shfl(w, i, kWave);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = __builtin_fmaf(wi, a.part_o[(i * all + row) * DH + lane + e * kWave], acc[e]);
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int64_t at = (q.t0 + c) * a.ldo + (int64_t)hq * DH + lane + e * kWave;
+    if constexpr (IO == kBF16)
+      static_cast<uint16_t*>(a.o)[at] = (uint16_t)f32_to_bf16_bits(acc[e] * inv);
+    else
+      static_cast<float*>(a.o)[at] = acc[e] * inv;
+  }
+}
+
+bool few_rows(const mhc_paged_desc& d) { return (int64_t)d.max_q * (d.Hq / d.Hk) <= kFewRows; }
+int row_tiles(const mhc_paged_desc& d) {
+  return few_rows(d) ? 1 : (int)(((int64_t)d.max_q * (d.Hq / d.Hk) + kRows - 1) / kRows);
+}
+
+// Splits of the keys: enough workgroups for every CU to hold two, none with
+// fewer than 128 keys (few rows) or 512 (many) of a full table.
+int splits_of(const mhc_paged_desc& d) {
+  const int64_t base = (int64_t)d.n_seqs * d.Hk * row_tiles(d);
+  const int64_t keys = (int64_t)d.max_pages * d.page_size;
+  int64_t want = (2 * device_cu_count() + base - 1) / base;
+  const int64_t most = (keys + (few_rows(d) ? 127 : 511)) / (few_rows(d) ? 128 : 512);
+  if (want > most) want = most;
+  if (want > kMaxSplits) want = kMaxSplits;
+  return want < 1 ? 1 : (int)want;
+}
+
+}  // namespace
+
+size_t attn_paged_workspace_bytes(const mhc_paged_desc& d) {
+  const int splits = splits_of(d);
+  if (splits == 1) return 0;
+  const size_t rows = (size_t)splits * (size_t)d.T * d.Hq;
+  return rows * d.Dh * sizeof(float) + rows * sizeof(float);
+}
+
+hipError_t launch_attn_paged(const mhc_paged_desc& d, const void* q, const void* kc, const void* vc, void* o, void* ws,
+                             hipStream_t s) {
+  PagedArgs a{};
+  a.T = d.T;
+  a.n = d.n_seqs;
+  a.max_q = d.max_q;
+  a.Hq = d.Hq;
+  a.Hk = d.Hk;
+  a.window = d.window;
+  a.max_pages = d.max_pages;
+  a.num_pages = (int)d.num_pages;
+  a.page_size = d.page_size;
+  a.fill = d.fill_outside;
+  a.splits = splits_of(d);
+  a.tiles = row_tiles(d);
+  a.by_page = div_of((uint32_t)d.page_size);
+  a.by_group = div_of((uint32_t)(d.Hq / d.Hk));
+  a.mod = {d.scale, d.softcap};
+  a.cu = d.cu_q;
+  a.prefix = d.prefix;
+  a.kv = d.kv_lens;
+  a.pages = d.pages;
+  a.slopes = d.slopes;
+  a.q = q;
+  a.kc = kc;
+  a.vc = vc;
+  a.o = o;
+  a.part_o = static_cast<float*>(ws);
+  a.part_l = a.part_o + (size_t)a.splits * (size_t)d.T * d.Hq * d.Dh;
+  a.ldq = d.ldq;
+  a.ldo = d.ldo;
+  const bool few = few_rows(d);
+  const dim3 grid((unsigned)((int64_t)d.n_seqs * d.Hk * a.tiles * a.splits));
+  hipError_t err = hipErrorInvalidValue;
+  dispatch_attn(d.io, d.Dh, d.softcap > 0.f || d.slopes != nullptr, [&](auto io_, auto dh_, auto mod_) {
+    constexpr int IO = decltype(io_)::value;
+    constexpr int DH = decltype(dh_)::value;
+    constexpr bool MOD = decltype(mod_)::value;
+    constexpr int row = Tile<IO, DH>::kRow;
+    // few: four waves' tiles, or their fp32 row states
+    constexpr int few_lds = 4 * 2 * kFewKeys * row > 4 * 32 * DH * 4 ? 4 * 2 * kFewKeys * row : 4 * 32 * DH * 4;
+    if (few)
+      MHC_LAUNCH((attn_paged_few_kernel<IO, DH, MOD>), grid, dim3(kThreads), few_lds, s, a);
+    else
+      MHC_LAUNCH((attn_paged_chunk_kernel<IO, DH, MOD>), grid, dim3(kThreads), 4 * kKeys * row, s, a);
+    err = hipGetLastError();
+    if (err != hipSuccess || a.splits == 1) return;
+    const int64_t rows = (int64_t)d.n_seqs * d.max_q * d.Hq;
+    MHC_LAUNCH((attn_paged_join_kernel<IO, DH>), dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a);
+    err = hipGetLastError();
+  });
+  return err;
+}
+
+}  // namespace mhc

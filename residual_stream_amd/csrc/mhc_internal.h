@@ -126,4 +126,24 @@ hipError_t launch_pre_bwd_mix(const mhc_desc& d, const void* dh, const void* x, 
                               const void* dxn, const float* H_res, void* dx, float* dphi, float* dbias,
                               float* dalpha, void* ws, hipStream_t s);
 
+// Query/key norm with the rotation; with slots the keys and values go to the
+// caches at ko and vo (n_slots token places each).
+hipError_t launch_qk_rope(const mhc_rope_desc& d, const void* q, const void* k, const void* v, const int32_t* pos,
+                          const double* freqs, const float* qw, const float* kw, void* qo, void* ko, void* vo,
+                          const int64_t* slots, int64_t n_slots, hipStream_t s);
+size_t qk_rope_bwd_workspace_bytes(const mhc_rope_desc& d);
+hipError_t launch_qk_rope_bwd(const mhc_rope_desc& d, const void* dqo, const void* dko, const void* q, const void* k,
+                              const int32_t* pos, const double* freqs, const float* qw, const float* kw, void* dq,
+                              void* dk, float* dqw, float* dkw, void* ws, hipStream_t s);
+
+// Attention over packed documents, its backward, and over a paged cache.
+hipError_t launch_attn(const mhc_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
+                       hipStream_t s);
+size_t attn_bwd_workspace_bytes(const mhc_attn_desc& d);
+hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void* q, const void* k, const void* v,
+                           const void* o, const float* lse, void* dq, void* dk, void* dv, void* ws, hipStream_t s);
+size_t attn_paged_workspace_bytes(const mhc_paged_desc& d);
+hipError_t launch_attn_paged(const mhc_paged_desc& d, const void* q, const void* kc, const void* vc, void* o, void* ws,
+                             hipStream_t s);
+
 }  // namespace mhc

@@ -43,6 +43,15 @@ ABI_FUNCTIONS = (
     "mhc_abi_version",
     "mhc_trace_kernel_events",
     "mhc_test_exchange_fault",
+    "mhc_qk_rope",
+    "mhc_qk_rope_bwd_workspace_bytes",
+    "mhc_qk_rope_bwd",
+    "mhc_qk_rope_cache",
+    "mhc_attn",
+    "mhc_attn_bwd_workspace_bytes",
+    "mhc_attn_bwd",
+    "mhc_attn_paged_workspace_bytes",
+    "mhc_attn_paged",
 )
 
 
@@ -58,6 +67,80 @@ class MhcDesc(ctypes.Structure):
         ("alpha_post", ctypes.c_float),
         ("alpha_res", ctypes.c_float),
         ("alpha", ctypes.c_void_p),
+    ]
+
+
+class MhcRopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("Hq", ctypes.c_int32),
+        ("Hk", ctypes.c_int32),
+        ("Dh", ctypes.c_int32),
+        ("R", ctypes.c_int32),
+        ("io", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("ldq", ctypes.c_int64),
+        ("ldk", ctypes.c_int64),
+        ("ldv", ctypes.c_int64),
+        ("ldq_out", ctypes.c_int64),
+        ("ldk_out", ctypes.c_int64),
+        ("ld_dq", ctypes.c_int64),
+        ("ld_dk", ctypes.c_int64),
+    ]
+
+
+class MhcAttnDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("Hq", ctypes.c_int32),
+        ("Hk", ctypes.c_int32),
+        ("Dh", ctypes.c_int32),
+        ("io", ctypes.c_int32),
+        ("n_docs", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("fill_outside", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("docs", ctypes.c_void_p),
+        ("prefix", ctypes.c_void_p),
+        ("slopes", ctypes.c_void_p),
+        ("ldq", ctypes.c_int64),
+        ("ldk", ctypes.c_int64),
+        ("ldv", ctypes.c_int64),
+        ("ldo", ctypes.c_int64),
+        ("ld_do", ctypes.c_int64),
+        ("ld_dq", ctypes.c_int64),
+        ("ld_dk", ctypes.c_int64),
+        ("ld_dv", ctypes.c_int64),
+    ]
+
+
+class MhcPagedDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("n_seqs", ctypes.c_int32),
+        ("max_q", ctypes.c_int32),
+        ("Hq", ctypes.c_int32),
+        ("Hk", ctypes.c_int32),
+        ("Dh", ctypes.c_int32),
+        ("io", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("fill_outside", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("cu_q", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+        ("pages", ctypes.c_void_p),
+        ("prefix", ctypes.c_void_p),
+        ("slopes", ctypes.c_void_p),
+        ("ldq", ctypes.c_int64),
+        ("ldo", ctypes.c_int64),
     ]
 
 
@@ -113,6 +196,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mhc_trace_kernel_events.argtypes = [_P, _P, ctypes.c_int, _P]
     lib.mhc_test_exchange_fault.restype = ctypes.c_int
     lib.mhc_test_exchange_fault.argtypes = [ctypes.c_int, ctypes.c_uint]
+    rope, dense, paged = (ctypes.POINTER(d) for d in (MhcRopeDesc, MhcAttnDesc, MhcPagedDesc))
+    for name, args in (("mhc_qk_rope", [rope] + [_P] * 9), ("mhc_qk_rope_bwd", [rope] + [_P] * 13 + [ctypes.c_size_t, _P]),
+                       ("mhc_qk_rope_cache", [rope] + [_P] * 11 + [ctypes.c_int64, _P]),
+                       ("mhc_attn", [dense] + [_P] * 6), ("mhc_attn_bwd", [dense] + [_P] * 10 + [ctypes.c_size_t, _P]),
+                       ("mhc_attn_paged", [paged] + [_P] * 5 + [ctypes.c_size_t, _P])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = args
+    for name, d in (("mhc_qk_rope_bwd", rope), ("mhc_attn_bwd", dense), ("mhc_attn_paged", paged)):
+        f = getattr(lib, name + "_workspace_bytes")
+        f.restype = ctypes.c_size_t
+        f.argtypes = [d]
     if path is None:
         _lib = lib
     return lib

@@ -1,0 +1,234 @@
+"""Masked attention over packed documents, forward and backward, against the
+fp64 oracle with elementwise bounds (oracle/attn_oracle.py), over types, head
+layouts, lengths and masks."""
+
+from __future__ import annotations
+
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attn_oracle as O
+from residual_stream_amd import attn
+
+from attn_testlib import bits, close, host, ints, rand, same
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+
+def _case(io, T, Hq, Hk, Dh, seed, **masks):
+    rng = np.random.default_rng(seed)
+    q, k, v, do = (rand(rng, (T, h, Dh), io, f) for h, f in ((Hq, 1.5), (Hk, 1.0), (Hk, 1.0), (Hq, 1.0)))
+    kw = dict(masks)
+    if kw.pop("alibi", False):
+        kw["slopes"] = torch.tensor([2.0 ** (-8.0 * (h + 1) / Hq) for h in range(Hq)], device="cuda")
+    ok = O.visible(T, kw.get("docs"), kw.get("causal", True), kw.get("prefix"), kw.get("window", 0))
+    i = np.arange(T)
+    ref = dict(io=io, scale=Dh ** -0.5, softcap=kw.get("softcap", 0.0),
+               slopes=None if "slopes" not in kw else host(kw["slopes"]))
+    for n in ("docs", "prefix"):
+        if kw.get(n) is not None:
+            kw[n] = ints(kw[n])
+    return (q, k, v, do), kw, ok, np.abs(i[:, None] - i[None]).astype(np.float64), ref
+
+
+# lengths around the tiles of 32, 64 and 128 rows and keys, and one key
+LENGTHS = [(1, 4, 2, 64), (2, 1, 1, 128), (31, 4, 4, 64), (33, 5, 1, 128), (64, 2, 2, 128), (65, 6, 2, 64),
+           (127, 3, 3, 128), (129, 8, 2, 64), (257, 5, 5, 64), (400, 10, 2, 128)]
+MASKS = {
+    "causal": {},
+    "full": dict(causal=False),
+    "capped": dict(softcap=5.0),
+    "distance": dict(alibi=True),
+    "capped_distance_full": dict(softcap=20.0, alibi=True, causal=False),
+    "window1": dict(window=1),
+    "window40": dict(window=40),
+    "prefix": dict(prefix=[50]),
+}
+
+
+def _run(io, T, Hq, Hk, Dh, seed, **masks):
+    (q, k, v, do), kw, ok, dist, ref = _case(io, T, Hq, Hk, Dh, seed, **masks)
+    o, lse = attn.mhc_attn(q, k, v, **kw)
+    grads = attn.mhc_attn_bwd(do, q, k, v, o, lse, **kw)
+    torch.cuda.synchronize()
+    ro, rl, eo = O.attention(host(q), host(k), host(v), ok, dist, **ref)
+    close("o", o, ro, eo)
+    seen = ok.any(-1)
+    assert np.isneginf(host(lse)[:, ~seen]).all()
+    el = O._scores(host(q)[:, 0], host(k)[:, 0], ok, dist, ref["scale"], ref["softcap"], None)[3].max() + 2.0 ** -20
+    assert np.abs(host(lse)[:, seen] - rl[:, seen]).max(initial=0.0) <= 4 * el + 2.0 ** -20 * np.abs(rl[:, seen]).max(initial=0.0)
+    rg, eg = O.attention_bwd(host(do), host(q), host(k), host(v), ok, dist, **ref)
+    for n, a, b, e in zip(("dq", "dk", "dv"), grads, rg, eg):
+        close(n, a, b, e)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Hq,Hk,Dh", LENGTHS)
+def test_lengths(io, T, Hq, Hk, Dh):
+    print(f"[attn] {io} T={T} {Hq}/{Hk}x{Dh}", file=sys.stderr, flush=True)
+    _run(io, T, Hq, Hk, Dh, seed=T)
+
+
+@pytest.mark.parametrize("io,Dh", [("bf16", 128), ("bf16", 64), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("mask", list(MASKS))
+def test_masks(io, Dh, mask):
+    print(f"[attn] {io} Dh={Dh} {mask}", file=sys.stderr, flush=True)
+    _run(io, 203, 4, 2, Dh, seed=7, **MASKS[mask])
+
+
+DOCS = {
+    "ragged": [0, 3, 3, 70, 71, 200, 330],
+    "rows_outside": [5, 40, 140, 300],
+    "all_empty": [0, 0, 0],
+    "single_tokens": list(range(0, 331)),
+    "empty_ends": [0, 0, 0, 330, 330, 330],
+}
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("docs", list(DOCS))
+@pytest.mark.parametrize("kind", ["causal", "full", "prefix", "window"])
+def test_documents(io, docs, kind):
+    print(f"[attn] {io} docs {docs} {kind}", file=sys.stderr, flush=True)
+    bounds = DOCS[docs]
+    n = len(bounds) - 1
+    masks = dict(docs=bounds)
+    if kind == "full":
+        masks["causal"] = False
+    elif kind == "prefix":  # none, negative, part, all, more than all
+        masks["prefix"] = [(0, -3, 20, 1, 64, 10 ** 9)[d % 6] for d in range(n)]
+    elif kind == "window":
+        masks["window"] = 17
+    _run(io, 330, 2, 1, 64, seed=11, **masks)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_strided_views_equal_contiguous_tensors(io):
+    T, Hq, Hk, Dh = 150, 6, 2, 64
+    rng = np.random.default_rng(3)
+    qkv, do = rand(rng, (T, (Hq + 2 * Hk) * Dh + 8), io), rand(rng, (T, Hq, Dh), io)
+    cut = lambda t, a, h: t[:, a * Dh:(a + h) * Dh].unflatten(1, (h, Dh))  # noqa: E731
+    q, k, v = cut(qkv, 0, Hq), cut(qkv, Hq, Hk), cut(qkv, Hq + Hk, Hk)
+    c = [t.contiguous() for t in (q, k, v)]
+    o, lse = attn.mhc_attn(q, k, v)
+    o2, lse2 = attn.mhc_attn(*c)
+    same("o", o, o2)
+    same("lse", lse, lse2)
+    d = torch.full_like(qkv, 7.0)
+    out = (cut(d, 0, Hq), cut(d, Hq, Hk), cut(d, Hq + Hk, Hk))
+    attn.mhc_attn_bwd(do, q, k, v, o, lse, out=out)
+    for n, a, b in zip(("dq", "dk", "dv"), out, attn.mhc_attn_bwd(do, *c, o, lse)):
+        same(n, a, b)
+    assert bool((d[:, (Hq + 2 * Hk) * Dh:] == 7.0).all()), "wrote between the rows"
+
+
+def test_rows_of_no_document_are_left_in_given_tensors():
+    T, Hq, Hk, Dh = 140, 2, 1, 64
+    rng = np.random.default_rng(5)
+    q, k, v, do = (rand(rng, (T, h, Dh), "bf16") for h in (Hq, Hk, Hk, Hq))
+    for t in (q, k, v, do):  # what they hold reaches nothing
+        t[:4] = float("nan")
+        t[100:] = float("nan")
+    docs = ints([4, 30, 30, 100])
+    full = lambda *s: torch.full(s, 3.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    o, lse = full(T, Hq, Dh), torch.full((Hq, T), 3.0, device="cuda")
+    attn.mhc_attn(q, k, v, docs=docs, out=(o, lse))
+    g = (full(T, Hq, Dh), full(T, Hk, Dh), full(T, Hk, Dh))
+    attn.mhc_attn_bwd(do, q, k, v, o, lse, docs=docs, out=g)
+    for t in (o, *g):
+        assert bool((t[:4] == 3.0).all()) and bool((t[100:] == 3.0).all())
+        assert bool(torch.isfinite(t[4:100].float()).all())
+    assert bool((lse[:, :4] == 3.0).all()) and bool((lse[:, 100:] == 3.0).all())
+    o2, lse2 = attn.mhc_attn(q, k, v, docs=docs)
+    g2 = attn.mhc_attn_bwd(do, q, k, v, o2, lse2, docs=docs)
+    for t, u in zip((o2, *g2), (o, *g)):
+        same("inside", t[4:100], u[4:100])
+        assert int(torch.count_nonzero(t[:4])) == 0 and int(torch.count_nonzero(t[100:])) == 0
+
+
+@pytest.mark.parametrize("docs", [[300, 200, 100], [-5, 10 ** 9], [10, 5, 400, -1, 60], [2 ** 31 - 1, -2 ** 31]])
+def test_unsorted_documents_stay_within_the_tensors(docs):
+    # meaningless results, but every access inside: the tensors next to them keep their values
+    T, Hq, Hk, Dh = 150, 2, 1, 64
+    rng = np.random.default_rng(6)
+    q, k, v, do = (rand(rng, (T, h, Dh), "bf16") for h in (Hq, Hk, Hk, Hq))
+    buf = torch.full((T + 256, Hq, Dh), 5.0, dtype=torch.bfloat16, device="cuda")
+    o, lse = buf[128:128 + T], torch.zeros((Hq, T), device="cuda")
+    attn.mhc_attn(q, k, v, docs=ints(docs), prefix=ints([10 ** 9] * (len(docs) - 1)), out=(o, lse))
+    attn.mhc_attn_bwd(do, q, k, v, o.contiguous(), lse, docs=ints(docs))
+    torch.cuda.synchronize()
+    assert bool((buf[:128] == 5.0).all()) and bool((buf[128 + T:] == 5.0).all())
+
+
+def test_large_scores_and_repeated_calls_give_the_same_bits():
+    T, Hq, Hk, Dh = 300, 4, 2, 128
+    rng = np.random.default_rng(8)
+    q, k, v, do = (rand(rng, (T, h, Dh), "bf16", f) for h, f in ((Hq, 12.0), (Hk, 12.0), (Hk, 1.0), (Hq, 1.0)))
+    first = None
+    for _ in range(3):
+        o, lse = attn.mhc_attn(q, k, v)
+        r = (o, lse, *attn.mhc_attn_bwd(do, q, k, v, o, lse))
+        assert all(bool(torch.isfinite(t.float()).all()) for t in r)
+        first = first or r
+        for a, b in zip(first, r):
+            assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("softcap,alibi", [(0.0, False), (3.0, True)])
+def test_gradients_against_differences(softcap, alibi):
+    """Directional derivative of Σ do·o in fp32 inputs: central differences of the
+    oracle's o (a step of 1e-5 is off by its square and 1e-11 / 1e-5) along the
+    kernel's gradient."""
+    (q, k, v, do), kw, ok, dist, ref = _case("f32", 70, 4, 2, 64, 21, softcap=softcap, alibi=alibi, docs=[0, 30, 70])
+    o, lse = attn.mhc_attn(q, k, v, **kw)
+    g = [host(t) for t in attn.mhc_attn_bwd(do, q, k, v, o, lse, **kw)]
+    rng = np.random.default_rng(0)
+    x = [host(t) for t in (q, k, v)]
+    for n in range(3):
+        u = rng.standard_normal(x[n].shape)
+        f = []
+        for s in (1e-5, -1e-5):
+            y = [a + s * u if i == n else a for i, a in enumerate(x)]
+            f.append((host(do) * O.attention(*y, ok, dist, **ref)[0]).sum())
+        num, ana = (f[0] - f[1]) / 2e-5, (g[n] * u).sum()
+        assert abs(num - ana) <= 1e-4 * np.sqrt((g[n] ** 2).sum()) + 1e-4 * abs(ana), ("qkv"[n], num, ana)
+
+
+def test_graph_replays_match_eager():
+    T, Hq, Hk, Dh = 200, 4, 2, 64
+    rng = np.random.default_rng(9)
+    sets = [[rand(rng, (T, h, Dh), "bf16") for h in (Hq, Hk, Hk, Hq)] for _ in range(3)]
+    q, k, v, do = (t.clone() for t in sets[0])
+    docs = ints([0, 60, 200])
+    out = [torch.empty_like(q), torch.empty((Hq, T), device="cuda")]
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+
+    def step():
+        attn.mhc_attn(q, k, v, docs=docs, softcap=10.0, out=tuple(out))
+        attn.mhc_attn_bwd(do, q, k, v, *out, docs=docs, softcap=10.0, out=tuple(grads))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for rep in range(4):
+        for t, s in zip((q, k, v, do), sets[rep % 3]):
+            t.copy_(s)
+        bound = [0, 20 * (rep + 1), 200]  # the masks are read at replay
+        docs.copy_(ints(bound))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (*out, *grads)]
+        o, lse = attn.mhc_attn(q, k, v, docs=docs, softcap=10.0)
+        ref = (o, lse, *attn.mhc_attn_bwd(do, q, k, v, o, lse, docs=docs, softcap=10.0))
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref):
+            same(f"replay {rep}", a, b)
