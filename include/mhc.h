@@ -348,20 +348,23 @@ typedef struct mhc_attn_desc {
   int64_t ld_do, ld_dq, ld_dk, ld_dv;
 } mhc_attn_desc;
 
-/* o_i = Σ_j softmax_j(s_ij) v_j, and lse[Hq][T] (fp32, natural log; NULL to
- * skip) for the backward. */
+/* o_i = Σ_j softmax_j(s_ij) v_j, and for the backward lse[Hq][T] (fp32,
+ * natural log; NULL to skip) and, bf16 only, o_rest[T][Hq][Dh] (one byte an
+ * element: the next eight bits of o after its rounding; NULL to skip). */
 mhc_status mhc_attn(const mhc_attn_desc* desc, const void* q, const void* k, const void* v, void* o, float* lse,
-                    hipStream_t stream);
+                    void* o_rest, hipStream_t stream);
 
 /* Bytes of device workspace mhc_attn_bwd needs; 0 for an invalid descriptor. */
 size_t mhc_attn_bwd_workspace_bytes(const mhc_attn_desc* desc);
 
-/* Backward of mhc_attn from its inputs, o and lse: dq[T][Hq][Dh], and dk, dv
- * [T][Hk][Dh] summed over the query heads that share a key head.  slopes are
- * constants.  Rows of no document as in the forward. */
+/* Backward of mhc_attn from its inputs, o, lse and o_rest: dq[T][Hq][Dh], and
+ * dk, dv [T][Hk][Dh] summed over the query heads that share a key head.  slopes
+ * are constants.  Rows of no document as in the forward.  Without o_rest (NULL)
+ * the rows' do·o is formed from the rounded o alone; that rounding is then the
+ * largest error of dq and dk where a row's weight lies on few keys. */
 mhc_status mhc_attn_bwd(const mhc_attn_desc* desc, const void* dout, const void* q, const void* k, const void* v,
-                        const void* o, const float* lse, void* dq, void* dk, void* dv, void* workspace,
-                        size_t workspace_bytes, hipStream_t stream);
+                        const void* o, const float* lse, const void* o_rest, void* dq, void* dk, void* dv,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Attention of new tokens over a paged cache [num_pages][page_size][Hk][Dh].
  * The rows of q and o are packed by sequence: sequence s has rows

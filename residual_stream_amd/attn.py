@@ -197,6 +197,22 @@ def _attn_desc(q, k, v, docs, causal, prefix, window, softcap, slopes, scale):
                        ldo=Hq * Dh, ld_do=Hq * Dh, ld_dq=Hq * Dh, ld_dk=Hk * Dh, ld_dv=Hk * Dh)
 
 
+def saved_floats(T: int, Hq: int, Dh: int, io: int) -> int:
+    """Length of the fp32 tensor in which :func:`mhc_attn` keeps what its backward
+    needs: the log-sum-exps [Hq, T] and, for bf16, the next eight bits of every
+    element of o (one byte each, from the next multiple of four floats on)."""
+    lse = -(-Hq * T // 4) * 4
+    return lse + (T * Hq * Dh // 4 if io == mhc.MHC_BF16 else 0)
+
+
+def _saved(name, saved, d, device):
+    """(lse, o_rest) pointers within the saved tensor."""
+    n = saved_floats(d.T, d.Hq, d.Dh, d.io)
+    _expect(name, saved, (n,), torch.float32, device)
+    lse = saved.data_ptr()
+    return ctypes.c_void_p(lse), (ctypes.c_void_p(lse + (-(-d.Hq * d.T // 4) * 16)) if d.io == mhc.MHC_BF16 else None)
+
+
 def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=0.0, slopes=None, scale=None, out=None,
              stream=None):
     """Attention of q[T,Hq,Dh] over k, v[T,Hk,Dh] (Dh 64 or 128) of a packed
@@ -207,23 +223,24 @@ def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=
     keys.  Scores are scale·q·k (scale: Dh^-0.5 if None), capped to
     softcap·tanh(·/softcap) if softcap > 0, minus slopes[h]·|i - j| (fp32 [Hq]).
 
-    Returns (o[T,Hq,Dh], lse[Hq,T] fp32).  Rows of no document come out as zeros
-    (lse -inf); in tensors passed as ``out=(o, lse or None)`` they are left as
-    they were."""
+    Returns (o[T,Hq,Dh], saved), ``saved`` an fp32 tensor of
+    :func:`saved_floats` elements for the backward; its first Hq·T are the rows'
+    log-sum-exps [Hq, T].  Rows of no document come out as zeros (lse -inf); in
+    tensors passed as ``out=(o, saved or None)`` they are left as they were."""
     lib = load()
     d = _attn_desc(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
     if out is None:
         d.fill_outside = 1
         out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               torch.empty((d.Hq, d.T), dtype=torch.float32, device=q.device))
-    o, lse = out
+               torch.empty(saved_floats(d.T, d.Hq, d.Dh, d.io), dtype=torch.float32, device=q.device))
+    o, saved = out
     d.ldo = _head_tensor("o", o, q.shape, q.dtype, q.device)
-    _expect("lse", lse, (d.Hq, d.T), torch.float32, q.device, optional=True)
-    _check(lib.mhc_attn(ctypes.byref(d), _p(q), _p(k), _p(v), _p(o), _p(lse), _stream(stream)), "mhc_attn")
+    lse, rest = (None, None) if saved is None else _saved("saved", saved, d, q.device)
+    _check(lib.mhc_attn(ctypes.byref(d), _p(q), _p(k), _p(v), _p(o), lse, rest, _stream(stream)), "mhc_attn")
     return out
 
 
-def mhc_attn_bwd(do, q, k, v, o, lse, *, docs=None, causal=True, prefix=None, window=0, softcap=0.0, slopes=None,
+def mhc_attn_bwd(do, q, k, v, o, saved, *, docs=None, causal=True, prefix=None, window=0, softcap=0.0, slopes=None,
                  scale=None, out=None, workspace=None, stream=None):
     """Backward of :func:`mhc_attn` from its inputs and results: returns (dq, dk,
     dv), dk and dv summed over the query heads that share a key head.  Rows of
@@ -234,7 +251,7 @@ def mhc_attn_bwd(do, q, k, v, o, lse, *, docs=None, causal=True, prefix=None, wi
     dv = q.device
     d.ld_do = _head_tensor("do", do, q.shape, q.dtype, dv)
     d.ldo = _head_tensor("o", o, q.shape, q.dtype, dv)
-    _expect("lse", lse, (d.Hq, d.T), torch.float32, dv)
+    lse, rest = _saved("saved", saved, d, dv)
     if out is None:
         d.fill_outside = 1
         out = tuple(torch.empty(t.shape, dtype=t.dtype, device=dv) for t in (q, k, v))
@@ -244,7 +261,7 @@ def mhc_attn_bwd(do, q, k, v, o, lse, *, docs=None, causal=True, prefix=None, wi
     if workspace is None and need:
         workspace = _workspace(need, dv)
     nbytes = _ws_bytes(workspace)
-    _check(lib.mhc_attn_bwd(ctypes.byref(d), _p(do), _p(q), _p(k), _p(v), _p(o), _p(lse), *(_p(g) for g in out),
+    _check(lib.mhc_attn_bwd(ctypes.byref(d), _p(do), _p(q), _p(k), _p(v), _p(o), lse, rest, *(_p(g) for g in out),
                             _p(workspace), nbytes, _stream(stream)), "mhc_attn_bwd")
     return out
 

@@ -215,7 +215,7 @@ mhc_status mhc_qk_rope_cache(const mhc_rope_desc* d, const void* q, const void* 
 }
 
 mhc_status mhc_attn(const mhc_attn_desc* d, const void* q, const void* k, const void* v, void* o, float* lse,
-                    hipStream_t stream) {
+                    void* o_rest, hipStream_t stream) {
   const mhc_status st = check_attn(d);
   if (st != MHC_OK) return st;
   if (d->T == 0) return MHC_OK;
@@ -223,15 +223,17 @@ mhc_status mhc_attn(const mhc_attn_desc* d, const void* q, const void* k, const 
   if (!stride_ok(d->ldq, d->Hq, d->Dh) || !stride_ok(d->ldk, d->Hk, d->Dh) || !stride_ok(d->ldv, d->Hk, d->Dh) ||
       !stride_ok(d->ldo, d->Hq, d->Dh))
     return MHC_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !optional(lse, 16)) return MHC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !optional(lse, 16) || !optional(o_rest, 16))
+    return MHC_ERR_INVALID_ARG;
+  if (d->io == MHC_F32 && o_rest != nullptr) return MHC_ERR_INVALID_ARG;
   const Heads in[3] = {heads(q, d->T, d->ldq, nq, d->io), heads(k, d->T, d->ldk, nk, d->io),
                        heads(v, d->T, d->ldv, nk, d->io)};
   const Heads out = heads(o, d->T, d->ldo, nq, d->io);
-  const Span l = bytes(lse, (size_t)d->Hq * d->T * 4);
-  if (meet(l, out.s)) return MHC_ERR_INVALID_ARG;
+  const Span l = bytes(lse, (size_t)d->Hq * d->T * 4), r = bytes(o_rest, (size_t)d->T * nq);
+  if (meet(l, out.s) || meet(r, out.s) || meet(l, r)) return MHC_ERR_INVALID_ARG;
   for (const Heads& i : in)
-    if (share(out, i) || meet(l, i.s)) return MHC_ERR_INVALID_ARG;
-  return from_hip(mhc::launch_attn(*d, q, k, v, o, lse, stream));
+    if (share(out, i) || meet(l, i.s) || meet(r, i.s)) return MHC_ERR_INVALID_ARG;
+  return from_hip(mhc::launch_attn(*d, q, k, v, o, lse, o_rest, stream));
 }
 
 size_t mhc_attn_bwd_workspace_bytes(const mhc_attn_desc* d) {
@@ -240,7 +242,7 @@ size_t mhc_attn_bwd_workspace_bytes(const mhc_attn_desc* d) {
 }
 
 mhc_status mhc_attn_bwd(const mhc_attn_desc* d, const void* dout, const void* q, const void* k, const void* v,
-                        const void* o, const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                        const void* o, const float* lse, const void* o_rest, void* dq, void* dk, void* dv, void* workspace,
                         size_t workspace_bytes, hipStream_t stream) {
   const mhc_status st = check_attn(d);
   if (st != MHC_OK) return st;
@@ -251,25 +253,27 @@ mhc_status mhc_attn_bwd(const mhc_attn_desc* d, const void* dout, const void* q,
       !stride_ok(d->ld_dk, d->Hk, d->Dh) || !stride_ok(d->ld_dv, d->Hk, d->Dh))
     return MHC_ERR_INVALID_ARG;
   if (!aligned16(dout) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
-      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !optional(o_rest, 16))
     return MHC_ERR_INVALID_ARG;
+  if (d->io == MHC_F32 && o_rest != nullptr) return MHC_ERR_INVALID_ARG;
   const Heads in[5] = {heads(q, d->T, d->ldq, nq, d->io), heads(k, d->T, d->ldk, nk, d->io),
                        heads(v, d->T, d->ldv, nk, d->io), heads(o, d->T, d->ldo, nq, d->io),
                        heads(dout, d->T, d->ld_do, nq, d->io)};
   const Heads out[3] = {heads(dq, d->T, d->ld_dq, nq, d->io), heads(dk, d->T, d->ld_dk, nk, d->io),
                         heads(dv, d->T, d->ld_dv, nk, d->io)};
   const Span l = bytes(lse, (size_t)d->Hq * d->T * 4), ws = bytes(workspace, workspace_bytes);
+  const Span r = bytes(o_rest, (size_t)d->T * nq);
   for (const Heads& x : out) {
     for (const Heads& i : in)
       if (share(x, i)) return MHC_ERR_INVALID_ARG;
-    if (meet(x.s, l) || meet(x.s, ws)) return MHC_ERR_INVALID_ARG;
+    if (meet(x.s, l) || meet(x.s, ws) || meet(x.s, r)) return MHC_ERR_INVALID_ARG;
   }
   if (share(out[0], out[1]) || share(out[0], out[2]) || share(out[1], out[2])) return MHC_ERR_INVALID_ARG;
   for (const Heads& i : in)
     if (meet(i.s, ws)) return MHC_ERR_INVALID_ARG;
-  if (meet(l, ws)) return MHC_ERR_INVALID_ARG;
+  if (meet(l, ws) || meet(r, ws)) return MHC_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, mhc::attn_bwd_workspace_bytes(*d))) return MHC_ERR_INVALID_ARG;
-  return from_hip(mhc::launch_attn_bwd(*d, dout, q, k, v, o, lse, dq, dk, dv, workspace, stream));
+  return from_hip(mhc::launch_attn_bwd(*d, dout, q, k, v, o, lse, o_rest, dq, dk, dv, workspace, stream));
 }
 
 size_t mhc_attn_paged_workspace_bytes(const mhc_paged_desc* d) {

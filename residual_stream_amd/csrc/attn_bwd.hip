@@ -22,16 +22,19 @@ attn::DocMask doc_mask(const mhc_attn_desc& d);
 namespace {
 
 constexpr int kRows = 128, kKeys = 64;   // dq: rows of a workgroup, keys of a tile
-constexpr int kKeyRows = 128, kQ = 64;   // dk, dv: keys of a workgroup, rows of a tile
+constexpr int kKeyRows = 128, kQ = 32;   // dk, dv: keys of a workgroup, rows of a tile
+constexpr int kMaxPieces = 16;
 
 struct BwdArgs {
   DocMask mask;
   ScoreMod mod;
   const void *q, *k, *v, *o, *dout;
   const float *slopes, *lse;
+  const uint8_t* rest;  // [T][Hq][Dh] or null
   float* delta;  // [Hq][T]
+  float* part;   // [pieces][dk, dv][T][Hk][Dh]
   void *dq, *dk, *dv;
-  int Hq, Hk, fill;
+  int Hq, Hk, fill, pieces;
   int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
 };
 
@@ -87,6 +90,8 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
       float ov[8], gv[8];
       load8<IO>(a.o, i * a.ldo + at, ov);
       load8<IO>(a.dout, i * a.lddo + at, gv);
+      if constexpr (IO == kBF16)
+        if (a.rest != nullptr) add_rest(a.rest, (int64_t)i * a.Hq * DH + at, ov);
 #pragma unroll
       for (int e = 0; e < 8; ++e) delta = __builtin_fmaf(ov[e], gv[e], delta);
     } else {
@@ -134,7 +139,6 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
         s = mma(T::row_frag(tk, 32 * b + c, n, h), qf[n], s);
         dp = mma(T::row_frag(tv, 32 * b + c, n, h), gf[n], dp);
       }
-      const int l0 = lo - key0 - 32 * b - 4 * h, h0 = hi - key0 - 32 * b - 4 * h;
       const float d0 = (float)(i - key0 - 32 * b - 4 * h);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -146,8 +150,16 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
           sc = s[r] * pre;
         float ds = exp2_fast(sc - lse2) * (dp[r] - delta);
         if constexpr (MOD) ds *= dcap;
-        if (partial) ds = k >= l0 && k < h0 ? ds : 0.f;
         s[r] = ds;
+      }
+      if (partial) {
+        int l0 = lo - key0 - 32 * b - 4 * h, h0 = hi - key0 - 32 * b - 4 * h;
+        keep_branch(l0, h0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int k = 8 * (r >> 2) + (r & 3);
+          s[r] = k >= l0 && k < h0 ? s[r] : 0.f;
+        }
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -167,28 +179,56 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
   }
 }
 
-// Keys: 128 of one key head a workgroup, 32 a wave (their key and value rows
-// in registers), over the rows that see them, head by head of the group, in
-// tiles of 64.  Scores here are S = Q·K^T with the wave's keys as columns.
+// Keys: 128 of one key head a workgroup, over the rows that see them, head by
+// head of the group, in tiles of 32.  Scores here are S = Q·K^T with the keys
+// as columns, so that P and dS are the B operands of dv^T = dO^T·P and
+// dk^T = Q^T·dS.
+//
+// Eight waves: a pair for every 32 keys, on the same SIMD.  The first wave of
+// a pair forms S and P and sums dv; the second forms dP, takes P from LDS one
+// tile later, and sums dk.  Each then holds one accumulator and one set of key
+// fragments, which leaves room for two waves a SIMD, one of which can use the
+// matrix cores while the other is at its exponentials (one wave a SIMD with
+// both sums: 2.4 ms at T = 8192, 40/8 heads of 128, bf16; two waves a SIMD
+// with both sums: spills, 4.2 ms).  One barrier a tile: tile n is in
+// use by the first waves while the second are at n - 1, so tiles have three
+// buffers and P two.
+//
+// The (head, row tile) steps of a key tile are cut into `pieces` for
+// workgroups of their own where the key tiles are too few to fill the chip;
+// each piece then leaves fp32 partial sums that attn_bwd_sum_kernel adds up in
+// order.
+constexpr int kKeyThreads = 512;
+
 template <int IO, int DH, bool MOD>
-__global__ __launch_bounds__(kThreads, 1) void attn_bwd_keys_kernel(BwdArgs a) {
+__global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kQ * T::kRow;
+  // three buffers of a row tile's q and dout, then P of two tiles for each pair
   extern __shared__ __attribute__((aligned(256))) char lds[];
   __shared__ int range[8];
-  __shared__ float stat[2][2][kQ];  // [buffer][lse in log 2 units, δ][row]
+  __shared__ float stat[3][2][kQ];  // [buffer][lse in log 2 units, δ][row]
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  const int pair = wave & 3;
+  const bool second = wave >= 4;  // (the same for the whole wave)
   const int G = a.Hq / a.Hk;
-  const int tile = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
-  const int j0 = tile * kKeyRows + wave * 32, j = j0 + c;
+  const int hk = blockIdx.x % a.Hk, piece = blockIdx.x / a.Hk % a.pieces, tile = blockIdx.x / a.Hk / a.pieces;
+  const int j0 = tile * kKeyRows + pair * 32, j = j0 + c;
 
   int ba, bb, lo, hi, wlo, whi;
   a.mask.bounds(j0, j0 + 31, ba, bb);
   const bool in_doc = a.mask.rows(j, ba, bb, lo, hi);
   wave_range(lo, hi, wlo, whi);
-  if (lane == 0) {
-    range[wave] = whi > 0 ? wlo : 0x7fffffff;
-    range[4 + wave] = whi;
+  if (!second && lane == 0) {
+    range[pair] = whi > 0 ? wlo : 0x7fffffff;
+    range[4 + pair] = whi;
+  }
+  Frag<IO> kf[DH / 16];  // keys, or the second wave's values
+  {
+    const void* p = second ? a.v : a.k;
+    const int64_t at = j * (second ? a.ldv : a.ldk) + (int64_t)hk * DH + 8 * h;
+#pragma unroll
+    for (int s = 0; s < DH / 16; ++s) kf[s] = j < a.mask.T ? load_frag<IO>(p, at + 16 * s) : zero_frag<IO>();
   }
   __syncthreads();
   int blo = min(min(range[0], range[1]), min(range[2], range[3]));
@@ -196,115 +236,199 @@ __global__ __launch_bounds__(kThreads, 1) void attn_bwd_keys_kernel(BwdArgs a) {
   if (bhi == 0) blo = 0;
   const bool live = in_doc && lo < hi;
 
-  Frag<IO> kf[DH / 16], vf[DH / 16];
-#pragma unroll
-  for (int s = 0; s < DH / 16; ++s) {
-    const int64_t at = (int64_t)hk * DH + 16 * s + 8 * h;
-    kf[s] = j < a.mask.T ? load_frag<IO>(a.k, j * a.ldk + at) : zero_frag<IO>();
-    vf[s] = j < a.mask.T ? load_frag<IO>(a.v, j * a.ldv + at) : zero_frag<IO>();
-  }
-  f32x16_t dk[DH / 32], dv[DH / 32];
+  f32x16_t acc[DH / 32];  // dv, or the second wave's dk
 #pragma unroll
   for (int b = 0; b < DH / 32; ++b)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) dk[b][r] = dv[b][r] = 0.f;
+    for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
   const float pre = a.mod.pre();
 
-  Stage<IO, DH, kQ> sq, sg;
-  float s_lse = 0.f, s_delta = 0.f;
+  // the first four waves bring q, the others dout
+  Stage<IO, DH, kQ> stage;
+  const int thread = threadIdx.x % kThreads;
+  float s_stat = 0.f;
   const int tiles = (bhi - blo + kQ - 1) / kQ, steps = tiles * G;
-  auto load = [&](int n) {
-    const int g = n / tiles, row0 = blo + (n - g * tiles) * kQ, hq = hk * G + g;
-    const int64_t head = (int64_t)hq * DH * T::kElem;
-    sq.load(static_cast<const char*>(a.q) + head + row0 * a.ldq * T::kElem, a.ldq, bhi - row0);
-    sg.load(static_cast<const char*>(a.dout) + head + row0 * a.lddo * T::kElem, a.lddo, bhi - row0);
-    if (threadIdx.x < kQ) {
-      const int row = row0 + threadIdx.x;
-      s_lse = row < bhi ? a.lse[(int64_t)hq * a.mask.T + row] * kLog2e : 0.f;
-      s_delta = row < bhi ? a.delta[(int64_t)hq * a.mask.T + row] : 0.f;
+  const int per = (steps + a.pieces - 1) / a.pieces;
+  const int first = min(piece * per, steps), last = min(first + per, steps);
+  auto load = [&](int g, int row0) {
+    const int hq = hk * G + g;
+    const int64_t ld = second ? a.lddo : a.ldq;
+    stage.load(static_cast<const char*>(second ? a.dout : a.q) + (row0 * ld + (int64_t)hq * DH) * T::kElem, ld, bhi - row0,
+               thread);
+    if (threadIdx.x < 2 * kQ) {  // lse by the first kQ threads, δ by the next
+      const int row = row0 + threadIdx.x % kQ;
+      const float* p = threadIdx.x < kQ ? a.lse : a.delta;
+      s_stat = row < bhi ? p[(int64_t)hq * a.mask.T + row] : 0.f;
+      if (threadIdx.x < kQ) s_stat *= kLog2e;
     }
   };
-  if (steps > 0) load(0);
-  for (int n = 0; n < steps; ++n) {
-    const int buf = n & 1, g = n / tiles, row0 = blo + (n - g * tiles) * kQ;
-    char* tq = lds + buf * 2 * kTile;
-    char* tg = tq + kTile;
-    sq.store(tq);
-    sg.store(tg);
-    if (threadIdx.x < kQ) {
-      stat[buf][0][threadIdx.x] = s_lse;
-      stat[buf][1][threadIdx.x] = s_delta;
-    }
-    if (n + 1 < steps) load(n + 1);
-    __syncthreads();
-    if (row0 >= whi || row0 + kQ <= wlo) continue;
-    const bool partial = __any(live && (lo > row0 || hi < row0 + kQ));
-    const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hk * G + g] * kLog2e : 0.f;
-#pragma unroll
-    for (int b = 0; b < kQ / 32; ++b) {
-      f32x16_t s, dp;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-#pragma unroll
-      for (int m = 0; m < DH / 16; ++m) {
-        s = mma(T::row_frag(tq, 32 * b + c, m, h), kf[m], s);
-        dp = mma(T::row_frag(tg, 32 * b + c, m, h), vf[m], dp);
+  // (head, row) of the tile that is loaded next, and of this wave's
+  int lg = first < last ? first / tiles : 0, lrow = blo + (first - lg * tiles) * kQ;
+  int wg = lg, wrow = lrow;
+  if (first < last) load(lg, lrow);
+  int buf = 0, prev = 0;  // buffer of tile n, of tile n - 1
+  for (int n = first; n < last + 1; ++n) {
+    if (n < last) {
+      char* tq = lds + buf * 2 * kTile;
+      stage.store(second ? tq + kTile : tq, thread);
+      if (threadIdx.x < 2 * kQ) stat[buf][threadIdx.x / kQ][threadIdx.x % kQ] = s_stat;
+      lrow += kQ;
+      if (lrow >= bhi) {
+        lrow = blo;
+        ++lg;
       }
-      const int l0 = lo - row0 - 32 * b - 4 * h, h0 = hi - row0 - 32 * b - 4 * h;
-      const float d0 = (float)(row0 + 32 * b + 4 * h - j);
+      if (n + 1 < last) load(lg, lrow);
+    }
+    __syncthreads();
+    const int mine = second ? prev : buf, row0 = wrow;
+    const bool mine_now = second ? n > first : n < last;
+    float* ps = reinterpret_cast<float*>(lds + 6 * kTile) + (((second ? n - 1 : n) & 1) * 4 + pair) * 16 * kWave;
+    prev = buf;
+    buf = buf == 2 ? 0 : buf + 1;
+    if (!mine_now) continue;
+    const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hk * G + wg] * kLog2e : 0.f;
+    wrow += kQ;
+    if (wrow >= bhi) {
+      wrow = blo;
+      ++wg;
+    }
+    if (row0 >= whi || row0 + kQ <= wlo) continue;  // (the pair's two waves alike)
+    const char* tq = lds + mine * 2 * kTile;
+    const char* tg = tq + kTile;
+    const bool partial = __any(live && (lo > row0 || hi < row0 + kQ));
+    const char* rows = second ? tg : tq;
+    const char* cols = second ? tq : tg;
+    f32x16_t s;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = 0.f;
+#pragma unroll
+    for (int m = 0; m < DH / 16; ++m) s = mma(T::row_frag(rows, c, m, h), kf[m], s);
+    if (!second) {
+      const float d0 = (float)(row0 + 4 * h - j);
+      f32x16_t out;  // P, or P times the capping's derivative, for the second wave
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
-        const float4 lse = *reinterpret_cast<const float4*>(&stat[buf][0][32 * b + 8 * r4 + 4 * h]);
-        const float4 del = *reinterpret_cast<const float4*>(&stat[buf][1][32 * b + 8 * r4 + 4 * h]);
-        const float lv[4] = {lse.x, lse.y, lse.z, lse.w}, dv4[4] = {del.x, del.y, del.z, del.w};
+        const float4 lse = *reinterpret_cast<const float4*>(&stat[mine][0][8 * r4 + 4 * h]);
+        const float lv[4] = {lse.x, lse.y, lse.z, lse.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 4 * r4 + e, k = 8 * r4 + e;
+          const int r = 4 * r4 + e;
           float sc, dcap = 1.f;
           if constexpr (MOD)
-            score<IO>(s[r], pre, a.mod, slope2, d0 + (float)k, sc, dcap);
+            score<IO>(s[r], pre, a.mod, slope2, d0 + (float)(8 * r4 + e), sc, dcap);
           else
             sc = s[r] * pre;
-          float p = exp2_fast(sc - lv[e]);
-          float ds = p * (dp[r] - dv4[e]);
-          if constexpr (MOD) ds *= dcap;
-          if (partial) {
-            const bool seen = k >= l0 && k < h0;
-            p = seen ? p : 0.f;
-            ds = seen ? ds : 0.f;
-          }
-          s[r] = p;
-          dp[r] = ds;
+          s[r] = exp2_fast(sc - lv[e]);
+          out[r] = s[r] * dcap;
+        }
+      }
+      if (partial) {
+        int l0 = lo - row0 - 4 * h, h0 = hi - row0 - 4 * h;
+        keep_branch(l0, h0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int k = 8 * (r >> 2) + (r & 3);
+          const bool seen = k >= l0 && k < h0;
+          s[r] = seen ? s[r] : 0.f;
+          out[r] = seen ? out[r] : 0.f;
         }
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const Frag<IO> p = frag_of<IO>(s, m), ds = frag_of<IO>(dp, m);
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(ps + (i * kWave + lane) * 4) = make_float4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+    } else {
 #pragma unroll
-        for (int d = 0; d < DH / 32; ++d) {
-          dv[d] = mma(T::col_frag(tg, 32 * b + 16 * m, d, lane), p, dv[d]);
-          dk[d] = mma(T::col_frag(tq, 32 * b + 16 * m, d, lane), ds, dk[d]);
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const float4 del = *reinterpret_cast<const float4*>(&stat[mine][1][8 * r4 + 4 * h]);
+        const float4 p = *reinterpret_cast<const float4*>(ps + (r4 * kWave + lane) * 4);
+        s[4 * r4] = p.x * (s[4 * r4] - del.x);
+        s[4 * r4 + 1] = p.y * (s[4 * r4 + 1] - del.y);
+        s[4 * r4 + 2] = p.z * (s[4 * r4 + 2] - del.z);
+        s[4 * r4 + 3] = p.w * (s[4 * r4 + 3] - del.w);
+      }
+      if (partial) {  // (0 times what is not finite)
+        int l0 = lo - row0 - 4 * h, h0 = hi - row0 - 4 * h;
+        keep_branch(l0, h0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int k = 8 * (r >> 2) + (r & 3);
+          s[r] = k >= l0 && k < h0 ? s[r] : 0.f;
         }
       }
     }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const Frag<IO> p = frag_of<IO>(s, m);
+#pragma unroll
+      for (int d = 0; d < DH / 32; ++d) acc[d] = mma(T::col_frag(cols, 16 * m, d, lane), p, acc[d]);
+    }
   }
-  if (j >= a.mask.T || (!in_doc && !a.fill)) return;
+  if (j >= a.mask.T) return;
+  if (!live) {
 #pragma unroll
-  for (int b = 0; b < DH / 32; ++b) {
-    if (!live)
+    for (int b = 0; b < DH / 32; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) dk[b][r] = dv[b][r] = 0.f;
-    store_block<IO>(a.dk, j * a.lddk + (int64_t)hk * DH, b, h, dk[b], a.mod.scale);
-    store_block<IO>(a.dv, j * a.lddv + (int64_t)hk * DH, b, h, dv[b], 1.f);
+      for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
+  }
+  const float f = second ? a.mod.scale : 1.f;
+  if (a.pieces > 1) {
+    const int64_t all = (int64_t)a.mask.T * a.Hk * DH, at = ((int64_t)j * a.Hk + hk) * DH;
+#pragma unroll
+    for (int b = 0; b < DH / 32; ++b) store_block<kF32>(a.part, (2 * piece + (second ? 0 : 1)) * all + at, b, h, acc[b], f);
+    return;
+  }
+  if (!in_doc && !a.fill) return;
+  const int64_t at = j * (second ? a.lddk : a.lddv) + (int64_t)hk * DH;
+#pragma unroll
+  for (int b = 0; b < DH / 32; ++b) store_block<IO>(second ? a.dk : a.dv, at, b, h, acc[b], f);
+}
+
+// Adds up the pieces' partial sums: eight elements a thread, one key row of
+// one of dk, dv a time.
+template <int IO>
+__global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdArgs a, int row) {
+  const int j = blockIdx.x;
+  if (!a.fill && a.mask.docs != nullptr) {
+    int ba, bb, s, e, p;
+    a.mask.bounds(j, j, ba, bb);
+    if (!a.mask.doc(j, ba, bb, s, e, p)) return;
+  }
+  const int64_t all = (int64_t)a.mask.T * row;
+  for (int t = threadIdx.x * 8; t < 2 * row; t += kThreads * 8) {
+    const int which = t >= row ? 1 : 0, e = t - which * row;
+    float sum[8], v[8];
+    load8<kF32>(a.part, which * all + (int64_t)j * row + e, sum);
+    for (int n = 1; n < a.pieces; ++n) {
+      load8<kF32>(a.part, (2 * n + which) * all + (int64_t)j * row + e, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    }
+    store8<IO>(which ? a.dv : a.dk, j * (which ? a.lddv : a.lddk) + e, sum);
   }
 }
 
 }  // namespace
 
-size_t attn_bwd_workspace_bytes(const mhc_attn_desc& d) { return (size_t)d.Hq * (size_t)d.T * sizeof(float); }
+static size_t delta_bytes(const mhc_attn_desc& d) { return ((size_t)d.Hq * (size_t)d.T * sizeof(float) + 255) / 256 * 256; }
+
+// Pieces of a key tile's steps: enough workgroups for two on every CU.
+static int pieces_of(const mhc_attn_desc& d) {
+  const int64_t base = (d.T + kKeyRows - 1) / kKeyRows * d.Hk;
+  int64_t n = (2 * device_cu_count() + base - 1) / base;
+  const int64_t steps = (d.T + kQ - 1) / kQ * (d.Hq / d.Hk);
+  if (n > (steps + 3) / 4) n = (steps + 3) / 4;  // at least four steps each
+  if (n > kMaxPieces) n = kMaxPieces;
+  return n < 1 ? 1 : (int)n;
+}
+
+size_t attn_bwd_workspace_bytes(const mhc_attn_desc& d) {
+  const int pieces = pieces_of(d);
+  return delta_bytes(d) + (pieces > 1 ? (size_t)pieces * 2 * (size_t)d.T * d.Hk * d.Dh * sizeof(float) : 0);
+}
 
 hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void* q, const void* k, const void* v,
-                           const void* o, const float* lse, void* dq, void* dk, void* dv, void* ws, hipStream_t s) {
+                           const void* o, const float* lse, const void* o_rest, void* dq, void* dk, void* dv, void* ws,
+                           hipStream_t s) {
   BwdArgs a{};
   a.mask = doc_mask(d);
   a.mod = {d.scale, d.softcap};
@@ -315,7 +439,10 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
   a.dout = dout;
   a.slopes = d.slopes;
   a.lse = lse;
+  a.rest = static_cast<const uint8_t*>(o_rest);
   a.delta = static_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(d));
+  a.pieces = pieces_of(d);
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
@@ -331,18 +458,20 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
   a.lddk = d.ld_dk;
   a.lddv = d.ld_dv;
   const dim3 rows((unsigned)((d.T + kRows - 1) / kRows * d.Hq));
-  const dim3 keys((unsigned)((d.T + kKeyRows - 1) / kKeyRows * d.Hk));
+  const dim3 keys((unsigned)((d.T + kKeyRows - 1) / kKeyRows * d.Hk * a.pieces));
   hipError_t err = hipErrorInvalidValue;
   dispatch_attn(d.io, d.Dh, d.softcap > 0.f || d.slopes != nullptr, [&](auto io_, auto dh_, auto mod_) {
     constexpr int IO = decltype(io_)::value;
     constexpr int DH = decltype(dh_)::value;
     constexpr bool MOD = decltype(mod_)::value;
-    constexpr int lds = 4 * 64 * Tile<IO, DH>::kRow;
-    static_assert(kKeys == 64 && kQ == 64, "tile bytes");
-    MHC_LAUNCH((attn_bwd_rows_kernel<IO, DH, MOD>), rows, dim3(kThreads), lds, s, a);
+    constexpr int row = Tile<IO, DH>::kRow;
+    MHC_LAUNCH((attn_bwd_rows_kernel<IO, DH, MOD>), rows, dim3(kThreads), 4 * kKeys * row, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return;
-    MHC_LAUNCH((attn_bwd_keys_kernel<IO, DH, MOD>), keys, dim3(kThreads), lds, s, a);
+    MHC_LAUNCH((attn_bwd_keys_kernel<IO, DH, MOD>), keys, dim3(kKeyThreads), 6 * kQ * row + 8 * 16 * kWave * 4, s, a);
+    err = hipGetLastError();
+    if (err != hipSuccess || a.pieces == 1) return;
+    MHC_LAUNCH((attn_bwd_sum_kernel<IO>), dim3((unsigned)d.T), dim3(kThreads), 0, s, a, d.Hk * d.Dh);
     err = hipGetLastError();
   });
   return err;

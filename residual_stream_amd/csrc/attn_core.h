@@ -88,16 +88,20 @@ __device__ __forceinline__ Frag<IO> frag_of(const f32x16_t& x, int half) {
 }
 
 // A tile of head rows in LDS, 16-byte chunks.  Chunk c of row r lies at place
-// c ^ swz(r) of the row, so that the eight lanes of a 16-byte read of one
-// chunk in eight rows, and the four rows of a transposing read, fall on
-// different banks.
+// c ^ swz(r) of the row.  Sixteen consecutive rows put one chunk on all 64
+// banks (reads along the rows), and four consecutive rows, a multiple of four
+// the first, put four neighbouring chunks on all of them (32 lanes of a
+// transposing read).  A swizzle that kept only eight rows apart cost half as
+// many cycles again on either read (SQ_LDS_BANK_CONFLICT).
 template <int IO, int DH>
 struct Tile {
   static constexpr int kElem = IoT<IO>::bytes;
   static constexpr int kRow = DH * kElem;      // bytes of a row
   static constexpr int kChunks = kRow / 16;    // 16-byte chunks of a row
   static constexpr int kPer = 16 / kElem;      // elements of a chunk
-  __device__ static __forceinline__ int swz(int r) { return kChunks >= 16 ? (2 * r) & 15 : r & 6; }
+  __device__ static __forceinline__ int swz(int r) {
+    return kChunks >= 16 ? (r & 3) << 2 | (r >> 2 & 3) : (r & 2) << 1 | (r >> 2 & 3);
+  }
   __device__ static __forceinline__ int at(int r, int c) { return r * kRow + ((c ^ swz(r)) << 4); }
 
   // Operand along the row: elements 16·s + 8·h + e of row r.
@@ -127,9 +131,9 @@ struct Tile {
       const int r = r0 + 4 * h + (i >> 2);
       const int col = 32 * blk + (lane & 16) + 4 * (i & 3);
       const int off = at(r, col >> 3) + (col & 7) * 2;
-      // rows r and r + 8 have the same swizzle
+      // swz(r + 8) = swz(r) ^ 2: two chunks, 32 bytes
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(t + off));
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(t + off + 8 * kRow));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(t + (off ^ 32) + 8 * kRow));
       const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
       f.w = u32x4_t{a.x, a.y, b.x, b.y};
     } else {
@@ -144,7 +148,7 @@ struct Tile {
   }
 };
 
-// Staging of R head rows by the workgroup: global memory to registers, then
+// Staging of R head rows by 256 threads: global memory to registers, then
 // registers to LDS, so that the next tile is on its way while this one is
 // used.  Thread i takes chunk i mod C of rows i/C, i/C + 256/C, ...
 template <int IO, int DH, int R>
@@ -152,26 +156,26 @@ struct Stage {
   using T = Tile<IO, DH>;
   static constexpr int kN = R * T::kChunks / kThreads;  // chunks a thread
   static constexpr int kStep = kThreads / T::kChunks;   // rows between a thread's chunks
-  static_assert(R * T::kChunks % kThreads == 0, "whole passes");
+  static_assert(R * T::kChunks % kThreads == 0 && kThreads % T::kChunks == 0, "whole passes");
   u32x4_t w[kN];
 
   // Rows base + 0 .. base + rows - 1, `ld` elements apart; the buffer's own
   // bounds check returns zeros for rows past the last.
-  __device__ __forceinline__ void load(const void* base, int64_t ld, int rows) {
+  __device__ __forceinline__ void load(const void* base, int64_t ld, int rows, int thread = threadIdx.x) {
     rows = min(rows, R);
     const int row_bytes = (int)(ld * T::kElem);
     const uint32_t bytes = rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)row_bytes + T::kRow : 0u;
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-    const uint32_t v0 = (uint32_t)(threadIdx.x / T::kChunks) * (uint32_t)row_bytes + (threadIdx.x % T::kChunks) * 16u;
+    const uint32_t v0 = (uint32_t)(thread / T::kChunks) * (uint32_t)row_bytes + (thread % T::kChunks) * 16u;
 #pragma unroll
     for (int n = 0; n < kN; ++n)
       w[n] = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(v0 + (uint32_t)(n * kStep) * (uint32_t)row_bytes), 0, 0);
   }
-  __device__ __forceinline__ void store(char* t) const {
+  __device__ __forceinline__ void store(char* t, int thread = threadIdx.x) const {
 #pragma unroll
     for (int n = 0; n < kN; ++n)
-      *reinterpret_cast<u32x4_t*>(t + T::at(threadIdx.x / T::kChunks + n * kStep, threadIdx.x % T::kChunks)) = w[n];
+      *reinterpret_cast<u32x4_t*>(t + T::at(thread / T::kChunks + n * kStep, thread % T::kChunks)) = w[n];
   }
 };
 
@@ -287,6 +291,10 @@ __device__ __forceinline__ float tanh_fast(float x) {
   return copysignf(fabsf(x) < 0.17f ? small : big, x);
 }
 
+// Ties a branch's compares to the branch: otherwise they are folded into
+// selects that every tile pays for, masked or not.
+__device__ __forceinline__ void keep_branch(int& a, int& b) { asm volatile("" : "+v"(a), "+v"(b)); }
+
 // How scores are formed from the products q·k, in units of log 2 so that exp2
 // serves: capped (cap·tanh(scale·x/cap), cap > 0), lowered by slope·distance.
 struct ScoreMod {
@@ -320,6 +328,38 @@ __device__ __forceinline__ void store_block(void* out, int64_t row, int blk, int
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
     else
       *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(a, b, c, d);
+  }
+}
+
+// The eight bits of an fp32 output that its bf16 rounding leaves out, as the
+// distance of the bit patterns in units of 2⁸ (neighbouring floats are
+// neighbouring integers): bf16 word << 16 plus rest << 8 gives the value back
+// to 2⁻¹⁶ of itself.
+__device__ __forceinline__ uint32_t rest_of(float x, uint32_t bf16_bits) {
+  const int d = (int)(__float_as_uint(x) - (bf16_bits << 16)) + 128;
+  const int r = d >> 8;
+  return (uint32_t)(r > 127 ? 127 : r) & 0xffu;
+}
+__device__ __forceinline__ void store_rest(uint8_t* rest, int64_t row, int blk, int h, const f32x16_t& x, float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float a = x[4 * i + 2 * e] * f, b = x[4 * i + 2 * e + 1] * f;
+      const uint32_t p = pack_bf16x2(a, b);
+      w |= (rest_of(a, p & 0xffffu) | rest_of(b, p >> 16) << 8) << (16 * e);
+    }
+    *reinterpret_cast<uint32_t*>(rest + row + 32 * blk + 8 * i + 4 * h) = w;
+  }
+}
+// Adds the rest to eight bf16 values widened to fp32.
+__device__ __forceinline__ void add_rest(const uint8_t* rest, int64_t at, float v[8]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(rest + at);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int r = (int)((e < 4 ? w.x : w.y) << (24 - 8 * (e & 3))) >> 24;
+    v[e] = __uint_as_float(__float_as_uint(v[e]) + ((uint32_t)r << 8));
   }
 }
 
@@ -372,7 +412,8 @@ __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH
     pre = 1.f;
   }
   if (partial) {
-    const int l0 = lo - key0 - 4 * h, h0 = hi - key0 - 4 * h;
+    int l0 = lo - key0 - 4 * h, h0 = hi - key0 - 4 * h;
+    keep_branch(l0, h0);
 #pragma unroll
     for (int b = 0; b < KB; ++b)
 #pragma unroll

@@ -29,7 +29,8 @@ struct FwdArgs {
   const void *q, *k, *v;
   const float* slopes;
   void* o;
-  float* lse;  // [Hq][T] or null
+  float* lse;     // [Hq][T] or null
+  uint8_t* rest;  // [T][Hq][Dh] or null (bf16)
   int Hq, Hk, fill;
   int64_t ldq, ldk, ldv, ldo;
 };
@@ -106,6 +107,8 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
 #pragma unroll
       for (int r = 0; r < 16; ++r) st.o[b][r] = 0.f;
     store_block<IO>(a.o, i * a.ldo + (int64_t)hq * DH, b, h, st.o[b], inv);
+    if constexpr (IO == kBF16)
+      if (a.rest != nullptr) store_rest(a.rest, ((int64_t)i * a.Hq + hq) * DH, b, h, st.o[b], inv);
   }
   if (a.lse != nullptr && h == 0)
     a.lse[(int64_t)hq * a.mask.T + i] = live ? (st.m + __log2f(l)) * kLn2 : -__builtin_inff();
@@ -125,7 +128,7 @@ attn::DocMask doc_mask(const mhc_attn_desc& d) {
 }
 
 hipError_t launch_attn(const mhc_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
-                       hipStream_t s) {
+                       void* o_rest, hipStream_t s) {
   FwdArgs a{};
   a.mask = doc_mask(d);
   a.mod = {d.scale, d.softcap};
@@ -135,6 +138,7 @@ hipError_t launch_attn(const mhc_attn_desc& d, const void* q, const void* k, con
   a.slopes = d.slopes;
   a.o = o;
   a.lse = lse;
+  a.rest = static_cast<uint8_t*>(o_rest);
   a.Hq = d.Hq;
   a.Hk = d.Hk;
   a.fill = d.fill_outside;

@@ -138,10 +138,11 @@ hipError_t launch_qk_rope_bwd(const mhc_rope_desc& d, const void* dqo, const voi
 
 // Attention over packed documents, its backward, and over a paged cache.
 hipError_t launch_attn(const mhc_attn_desc& d, const void* q, const void* k, const void* v, void* o, float* lse,
-                       hipStream_t s);
+                       void* o_rest, hipStream_t s);
 size_t attn_bwd_workspace_bytes(const mhc_attn_desc& d);
 hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void* q, const void* k, const void* v,
-                           const void* o, const float* lse, void* dq, void* dk, void* dv, void* ws, hipStream_t s);
+                           const void* o, const float* lse, const void* o_rest, void* dq, void* dk, void* dv, void* ws,
+                           hipStream_t s);
 size_t attn_paged_workspace_bytes(const mhc_paged_desc& d);
 hipError_t launch_attn_paged(const mhc_paged_desc& d, const void* q, const void* kc, const void* vc, void* o, void* ws,
                              hipStream_t s);

@@ -199,7 +199,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     rope, dense, paged = (ctypes.POINTER(d) for d in (MhcRopeDesc, MhcAttnDesc, MhcPagedDesc))
     for name, args in (("mhc_qk_rope", [rope] + [_P] * 9), ("mhc_qk_rope_bwd", [rope] + [_P] * 13 + [ctypes.c_size_t, _P]),
                        ("mhc_qk_rope_cache", [rope] + [_P] * 11 + [ctypes.c_int64, _P]),
-                       ("mhc_attn", [dense] + [_P] * 6), ("mhc_attn_bwd", [dense] + [_P] * 10 + [ctypes.c_size_t, _P]),
+                       ("mhc_attn", [dense] + [_P] * 7), ("mhc_attn_bwd", [dense] + [_P] * 11 + [ctypes.c_size_t, _P]),
                        ("mhc_attn_paged", [paged] + [_P] * 5 + [ctypes.c_size_t, _P])):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = args

@@ -11,7 +11,7 @@ import pytest
 import torch
 
 from oracle import attn_oracle as O
-from residual_stream_amd import attn
+from residual_stream_amd import attn, mhc
 
 from attn_testlib import bits, close, host, ints, rand, same
 
@@ -37,6 +37,14 @@ def _case(io, T, Hq, Hk, Dh, seed, **masks):
     return (q, k, v, do), kw, ok, np.abs(i[:, None] - i[None]).astype(np.float64), ref
 
 
+def _lse(saved, Hq, T):
+    return saved[:Hq * T].view(Hq, T)
+
+
+def _new_saved(T, Hq, Dh, io, value=0.0):
+    return torch.full((attn.saved_floats(T, Hq, Dh, mhc.MHC_BF16 if io == "bf16" else mhc.MHC_F32),), value, device="cuda")
+
+
 # lengths around the tiles of 32, 64 and 128 rows and keys, and one key
 LENGTHS = [(1, 4, 2, 64), (2, 1, 1, 128), (31, 4, 4, 64), (33, 5, 1, 128), (64, 2, 2, 128), (65, 6, 2, 64),
            (127, 3, 3, 128), (129, 8, 2, 64), (257, 5, 5, 64), (400, 10, 2, 128)]
@@ -54,8 +62,9 @@ MASKS = {
 
 def _run(io, T, Hq, Hk, Dh, seed, **masks):
     (q, k, v, do), kw, ok, dist, ref = _case(io, T, Hq, Hk, Dh, seed, **masks)
-    o, lse = attn.mhc_attn(q, k, v, **kw)
-    grads = attn.mhc_attn_bwd(do, q, k, v, o, lse, **kw)
+    o, saved = attn.mhc_attn(q, k, v, **kw)
+    grads = attn.mhc_attn_bwd(do, q, k, v, o, saved, **kw)
+    lse = _lse(saved, Hq, T)
     torch.cuda.synchronize()
     ro, rl, eo = O.attention(host(q), host(k), host(v), ok, dist, **ref)
     close("o", o, ro, eo)
@@ -119,7 +128,7 @@ def test_strided_views_equal_contiguous_tensors(io):
     o, lse = attn.mhc_attn(q, k, v)
     o2, lse2 = attn.mhc_attn(*c)
     same("o", o, o2)
-    same("lse", lse, lse2)
+    same("saved", lse[:Hq * T], lse2[:Hq * T])
     d = torch.full_like(qkv, 7.0)
     out = (cut(d, 0, Hq), cut(d, Hq, Hk), cut(d, Hq + Hk, Hk))
     attn.mhc_attn_bwd(do, q, k, v, o, lse, out=out)
@@ -137,14 +146,15 @@ def test_rows_of_no_document_are_left_in_given_tensors():
         t[100:] = float("nan")
     docs = ints([4, 30, 30, 100])
     full = lambda *s: torch.full(s, 3.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
-    o, lse = full(T, Hq, Dh), torch.full((Hq, T), 3.0, device="cuda")
+    o, lse = full(T, Hq, Dh), _new_saved(T, Hq, Dh, "bf16", 3.0)
     attn.mhc_attn(q, k, v, docs=docs, out=(o, lse))
     g = (full(T, Hq, Dh), full(T, Hk, Dh), full(T, Hk, Dh))
     attn.mhc_attn_bwd(do, q, k, v, o, lse, docs=docs, out=g)
     for t in (o, *g):
         assert bool((t[:4] == 3.0).all()) and bool((t[100:] == 3.0).all())
         assert bool(torch.isfinite(t[4:100].float()).all())
-    assert bool((lse[:, :4] == 3.0).all()) and bool((lse[:, 100:] == 3.0).all())
+    for rows in (slice(0, 4), slice(100, T)):
+        assert bool((_lse(lse, Hq, T)[:, rows] == 3.0).all())
     o2, lse2 = attn.mhc_attn(q, k, v, docs=docs)
     g2 = attn.mhc_attn_bwd(do, q, k, v, o2, lse2, docs=docs)
     for t, u in zip((o2, *g2), (o, *g)):
@@ -159,7 +169,7 @@ def test_unsorted_documents_stay_within_the_tensors(docs):
     rng = np.random.default_rng(6)
     q, k, v, do = (rand(rng, (T, h, Dh), "bf16") for h in (Hq, Hk, Hk, Hq))
     buf = torch.full((T + 256, Hq, Dh), 5.0, dtype=torch.bfloat16, device="cuda")
-    o, lse = buf[128:128 + T], torch.zeros((Hq, T), device="cuda")
+    o, lse = buf[128:128 + T], _new_saved(T, Hq, Dh, "bf16")
     attn.mhc_attn(q, k, v, docs=ints(docs), prefix=ints([10 ** 9] * (len(docs) - 1)), out=(o, lse))
     attn.mhc_attn_bwd(do, q, k, v, o.contiguous(), lse, docs=ints(docs))
     torch.cuda.synchronize()
@@ -172,8 +182,8 @@ def test_large_scores_and_repeated_calls_give_the_same_bits():
     q, k, v, do = (rand(rng, (T, h, Dh), "bf16", f) for h, f in ((Hq, 12.0), (Hk, 12.0), (Hk, 1.0), (Hq, 1.0)))
     first = None
     for _ in range(3):
-        o, lse = attn.mhc_attn(q, k, v)
-        r = (o, lse, *attn.mhc_attn_bwd(do, q, k, v, o, lse))
+        o, saved = attn.mhc_attn(q, k, v)
+        r = (o, _lse(saved, Hq, T), *attn.mhc_attn_bwd(do, q, k, v, o, saved))
         assert all(bool(torch.isfinite(t.float()).all()) for t in r)
         first = first or r
         for a, b in zip(first, r):
@@ -206,7 +216,7 @@ def test_graph_replays_match_eager():
     sets = [[rand(rng, (T, h, Dh), "bf16") for h in (Hq, Hk, Hk, Hq)] for _ in range(3)]
     q, k, v, do = (t.clone() for t in sets[0])
     docs = ints([0, 60, 200])
-    out = [torch.empty_like(q), torch.empty((Hq, T), device="cuda")]
+    out = [torch.zeros_like(q), _new_saved(T, Hq, Dh, "bf16")]
     grads = [torch.empty_like(t) for t in (q, k, v)]
 
     def step():

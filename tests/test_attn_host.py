@@ -34,7 +34,7 @@ def _rope(**kw):
 
 
 def _attn(**kw):
-    d = dict(T=4, Hq=4, Hk=2, Dh=64, io=mhc.MHC_F32, n_docs=1, causal=1, window=0, scale=0.125, softcap=0.0, ldq=256, ldk=128,
+    d = dict(T=4, Hq=4, Hk=2, Dh=64, io=mhc.MHC_BF16, n_docs=1, causal=1, window=0, scale=0.125, softcap=0.0, ldq=256, ldk=128,
              ldv=128, ldo=256, ld_do=256, ld_dq=256, ld_dk=128, ld_dv=128)
     d.update(kw)
     return mhc.MhcAttnDesc(**d)
@@ -54,8 +54,8 @@ def _calls(lib, name, d, ptrs, ws=(None, 0)):
     return getattr(lib, name)(ctypes.byref(d), *ptrs, *tail)
 
 
-N_PTRS = {"mhc_qk_rope": (_rope, 8), "mhc_qk_rope_bwd": (_rope, 12), "mhc_qk_rope_cache": (_rope, 11), "mhc_attn": (_attn, 5),
-          "mhc_attn_bwd": (_attn, 9), "mhc_attn_paged": (_paged, 4)}
+N_PTRS = {"mhc_qk_rope": (_rope, 8), "mhc_qk_rope_bwd": (_rope, 12), "mhc_qk_rope_cache": (_rope, 11), "mhc_attn": (_attn, 6),
+          "mhc_attn_bwd": (_attn, 10), "mhc_attn_paged": (_paged, 4)}
 NO_GPU = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses are only passed where no GPU exists")
 
 
@@ -85,9 +85,9 @@ def test_bad_fields(lib, make, name, field, value, expect):
 
 def test_masks_that_exclude_each_other(lib):
     for d in (_attn(causal=0, window=3), _attn(causal=0, prefix=FAKE[0]), _attn(window=3, prefix=FAKE[0])):
-        assert _calls(lib, "mhc_attn", d, [None] * 5) == mhc.MHC_ERR_UNSUPPORTED
+        assert _calls(lib, "mhc_attn", d, [None] * 6) == mhc.MHC_ERR_UNSUPPORTED
     assert _calls(lib, "mhc_attn_paged", _paged(window=3, prefix=FAKE[0]), [None] * 4) == mhc.MHC_ERR_UNSUPPORTED
-    assert _calls(lib, "mhc_attn", _attn(docs=FAKE[0], n_docs=0), [None] * 5) == mhc.MHC_ERR_INVALID_ARG
+    assert _calls(lib, "mhc_attn", _attn(docs=FAKE[0], n_docs=0), [None] * 6) == mhc.MHC_ERR_INVALID_ARG
 
 
 @NO_GPU
@@ -95,8 +95,8 @@ def test_masks_that_exclude_each_other(lib):
 def test_null_misaligned_and_overlapping_pointers(lib, name):
     make, n = N_PTRS[name]
     ws = (FAKE[15], 1 << 20)
-    may_be_null = {"mhc_qk_rope": (4, 5), "mhc_qk_rope_bwd": (6, 7, 10, 11), "mhc_qk_rope_cache": (5, 6), "mhc_attn": (4,),
-                   "mhc_attn_bwd": (), "mhc_attn_paged": ()}[name]
+    may_be_null = {"mhc_qk_rope": (4, 5), "mhc_qk_rope_bwd": (6, 7, 10, 11), "mhc_qk_rope_cache": (5, 6), "mhc_attn": (4, 5),
+                   "mhc_attn_bwd": (6,), "mhc_attn_paged": ()}[name]
     for i in range(n):
         ptrs = [ctypes.c_void_p(p) for p in FAKE[:n]]
         if i not in may_be_null:
@@ -105,12 +105,19 @@ def test_null_misaligned_and_overlapping_pointers(lib, name):
         ptrs[i] = ctypes.c_void_p(FAKE[i] + 2)
         assert _calls(lib, name, make(), ptrs, ws) == mhc.MHC_ERR_INVALID_ARG, (name, i)
     outs = {"mhc_qk_rope": (6, 7), "mhc_qk_rope_bwd": (8, 9), "mhc_qk_rope_cache": (7, 8, 9), "mhc_attn": (3,),
-            "mhc_attn_bwd": (6, 7, 8), "mhc_attn_paged": (3,)}[name]
+            "mhc_attn_bwd": (7, 8, 9), "mhc_attn_paged": (3,)}[name]
     for o in outs:
         for other in [0, 1] + [x for x in outs if x != o]:
             ptrs = [ctypes.c_void_p(p) for p in FAKE[:n]]
             ptrs[o] = ctypes.c_void_p(FAKE[other] + 16)
             assert _calls(lib, name, make(), ptrs, ws) == mhc.MHC_ERR_INVALID_ARG, (name, o, other)
+
+
+@NO_GPU
+def test_the_rest_of_o_is_for_bf16_only(lib):
+    p = [ctypes.c_void_p(x) for x in FAKE]
+    for name in ("mhc_attn", "mhc_attn_bwd"):
+        assert _calls(lib, name, _attn(io=mhc.MHC_F32), p[:N_PTRS[name][1]], (FAKE[15], 1 << 20)) == mhc.MHC_ERR_INVALID_ARG
 
 
 @NO_GPU
@@ -122,7 +129,7 @@ def test_workspaces_and_strides(lib):
             assert _calls(lib, name, make(), p[:n], ws) == mhc.MHC_ERR_INVALID_ARG
     for field in ("ldq", "ldk", "ldv", "ldo"):
         for value in (64, 257, 1 << 23, -256):
-            assert _calls(lib, "mhc_attn", _attn(**{field: value}), p[:5]) == mhc.MHC_ERR_INVALID_ARG
+            assert _calls(lib, "mhc_attn", _attn(**{field: value}), p[:6]) == mhc.MHC_ERR_INVALID_ARG
 
 
 def test_workspace_queries(lib):
@@ -139,8 +146,8 @@ def test_workspace_queries(lib):
 def test_empty_calls_launch_nothing(lib):
     assert _calls(lib, "mhc_qk_rope", _rope(T=0), [None] * 8) == mhc.MHC_OK
     assert _calls(lib, "mhc_qk_rope_bwd", _rope(T=0), [None] * 12) == mhc.MHC_OK
-    assert _calls(lib, "mhc_attn", _attn(T=0), [None] * 5) == mhc.MHC_OK
-    assert _calls(lib, "mhc_attn_bwd", _attn(T=0), [None] * 9) == mhc.MHC_OK
+    assert _calls(lib, "mhc_attn", _attn(T=0), [None] * 6) == mhc.MHC_OK
+    assert _calls(lib, "mhc_attn_bwd", _attn(T=0), [None] * 10) == mhc.MHC_OK
     assert _calls(lib, "mhc_attn_paged", _paged(T=0, n_seqs=0), [None] * 4) == mhc.MHC_OK
 
 
