@@ -56,9 +56,9 @@ template <int IO, int DH, bool MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_kernel(BwdArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
-  extern __shared__ __attribute__((aligned(256))) char lds[];
+  extern __shared__ __attribute__((aligned(512))) char lds[];
   __shared__ int range[8];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   const int G = a.Hq / a.Hk;
   const int nt = (a.mask.T + kRows - 1) / kRows;
   const int tile = nt - 1 - (int)(blockIdx.x / a.Hq), x = blockIdx.x % a.Hq;
@@ -107,6 +107,9 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
   const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
   Stage<IO, DH, kKeys> sk, sv;
   const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hq] * kLog2e : 0.f;
+  settle(qf);
+  settle(gf);
+  asm volatile("" : "+v"(lse2), "+v"(delta));
   const float pre = a.mod.pre();
   f32x16_t acc[DH / 32];
 #pragma unroll
@@ -129,16 +132,16 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
     __syncthreads();
     if (key0 >= whi || next <= wlo) continue;
     const bool partial = __any(live && (lo > key0 || hi < next));
+    const uint32_t ra = T::row_addr(lds_addr(tk), c, h), ca = T::col_addr(lds_addr(tk), lane);
 #pragma unroll
     for (int b = 0; b < kKeys / 32; ++b) {
       f32x16_t s, dp;
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-#pragma unroll
-      for (int n = 0; n < DH / 16; ++n) {
-        s = mma(T::row_frag(tk, 32 * b + c, n, h), qf[n], s);
-        dp = mma(T::row_frag(tv, 32 * b + c, n, h), gf[n], dp);
-      }
+      each<DH / 16>([&](auto n) {
+        s = mma(T::template row_frag<n>(ra, 32 * b * T::kRow), qf[n], s);
+        dp = mma(T::template row_frag<n>(ra, kTile + 32 * b * T::kRow), gf[n], dp);
+      });
       const float d0 = (float)(i - key0 - 32 * b - 4 * h);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -164,8 +167,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const Frag<IO> ds = frag_of<IO>(s, n);
-#pragma unroll
-        for (int d = 0; d < DH / 32; ++d) acc[d] = mma(T::col_frag(tk, 32 * b + 16 * n, d, lane), ds, acc[d]);
+        each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, (32 * b + 16 * n) * T::kRow), ds, acc[d]); });
       }
     }
   }
@@ -205,10 +207,10 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
   using T = Tile<IO, DH>;
   constexpr int kTile = kQ * T::kRow;
   // three buffers of a row tile's q and dout, then P of two tiles for each pair
-  extern __shared__ __attribute__((aligned(256))) char lds[];
+  extern __shared__ __attribute__((aligned(512))) char lds[];
   __shared__ int range[8];
   __shared__ float stat[3][2][kQ];  // [buffer][lse in log 2 units, δ][row]
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   const int pair = wave & 3;
   const bool second = wave >= 4;  // (the same for the whole wave)
   const int G = a.Hq / a.Hk;
@@ -229,6 +231,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
     const int64_t at = j * (second ? a.ldv : a.ldk) + (int64_t)hk * DH + 8 * h;
 #pragma unroll
     for (int s = 0; s < DH / 16; ++s) kf[s] = j < a.mask.T ? load_frag<IO>(p, at + 16 * s) : zero_frag<IO>();
+    settle(kf);
   }
   __syncthreads();
   int blo = min(min(range[0], range[1]), min(range[2], range[3]));
@@ -259,7 +262,6 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
       const int row = row0 + threadIdx.x % kQ;
       const float* p = threadIdx.x < kQ ? a.lse : a.delta;
       s_stat = row < bhi ? p[(int64_t)hq * a.mask.T + row] : 0.f;
-      if (threadIdx.x < kQ) s_stat *= kLog2e;
     }
   };
   // (head, row) of the tile that is loaded next, and of this wave's
@@ -271,7 +273,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
     if (n < last) {
       char* tq = lds + buf * 2 * kTile;
       stage.store(second ? tq + kTile : tq, thread);
-      if (threadIdx.x < 2 * kQ) stat[buf][threadIdx.x / kQ][threadIdx.x % kQ] = s_stat;
+      if (threadIdx.x < 2 * kQ) stat[buf][threadIdx.x / kQ][threadIdx.x % kQ] = threadIdx.x < kQ ? s_stat * kLog2e : s_stat;
       lrow += kQ;
       if (lrow >= bhi) {
         lrow = blo;
@@ -293,16 +295,14 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
       ++wg;
     }
     if (row0 >= whi || row0 + kQ <= wlo) continue;  // (the pair's two waves alike)
-    const char* tq = lds + mine * 2 * kTile;
-    const char* tg = tq + kTile;
+    // the first wave reads the rows of q and the columns of dout, the second the reverse
+    const uint32_t tq = lds_addr(lds) + mine * 2 * kTile;
+    const uint32_t ra = T::row_addr(second ? tq + kTile : tq, c, h), ca = T::col_addr(second ? tq : tq + kTile, lane);
     const bool partial = __any(live && (lo > row0 || hi < row0 + kQ));
-    const char* rows = second ? tg : tq;
-    const char* cols = second ? tq : tg;
     f32x16_t s;
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[r] = 0.f;
-#pragma unroll
-    for (int m = 0; m < DH / 16; ++m) s = mma(T::row_frag(rows, c, m, h), kf[m], s);
+    each<DH / 16>([&](auto m) { s = mma(T::template row_frag<m>(ra, 0), kf[m], s); });
     if (!second) {
       const float d0 = (float)(row0 + 4 * h - j);
       f32x16_t out;  // P, or P times the capping's derivative, for the second wave
@@ -359,8 +359,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const Frag<IO> p = frag_of<IO>(s, m);
-#pragma unroll
-      for (int d = 0; d < DH / 32; ++d) acc[d] = mma(T::col_frag(cols, 16 * m, d, lane), p, acc[d]);
+      each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, 16 * m * T::kRow), p, acc[d]); });
     }
   }
   if (j >= a.mask.T) return;

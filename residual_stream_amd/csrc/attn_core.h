@@ -27,6 +27,9 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) const u32x4_t* lds_u32x4_t;
+typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_t;
+typedef __attribute__((address_space(3))) const float* lds_float_t;
 
 // Eight elements of an operand.
 template <int IO>
@@ -72,6 +75,25 @@ __device__ __forceinline__ Frag<IO> zero_frag() {
   return f;
 }
 
+// Waits for fragments loaded from global memory here and now.  Without it the
+// first use inside a loop waits, every time round, for whatever loads are in
+// flight by then: the next tile's.
+template <int IO, int N>
+__device__ __forceinline__ void settle(Frag<IO> (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (IO == kBF16) {
+      asm volatile("" : "+v"(f[i].w));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(f[i].v[e]));
+    }
+  }
+}
+
+// The wave's number, known to be the same for all its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
+
 // The operand formed from accumulator elements 8·half .. 8·half + 7 of x.
 // bf16: each is rounded once, to the type the matrix cores take.
 template <int IO>
@@ -104,49 +126,81 @@ struct Tile {
   }
   __device__ static __forceinline__ int at(int r, int c) { return r * kRow + ((c ^ swz(r)) << 4); }
 
-  // Operand along the row: elements 16·s + 8·h + e of row r.
-  __device__ static __forceinline__ Frag<IO> row_frag(const char* t, int r, int s, int h) {
+  // Operand along the row: elements 16·s + 8·h + e of row c (+ a multiple of
+  // 16, as a byte offset `off`).  `at0` = row_addr(tile, c, h); the chunks of a
+  // row differ from it by an exclusive or with a constant (tiles start at
+  // multiples of a row, 512 bytes at most).
+  __device__ static __forceinline__ uint32_t row_addr(uint32_t tile, int c, int h) {
+    return tile + c * kRow + (((kElem == 2 ? h : 2 * h) ^ swz(c)) << 4);
+  }
+  template <int S>
+  __device__ static __forceinline__ Frag<IO> row_frag(uint32_t at0, int off) {
     Frag<IO> f;
     if constexpr (IO == kBF16) {
-      f.w = *reinterpret_cast<const u32x4_t*>(t + at(r, 2 * s + h));
+      f.w = *reinterpret_cast<lds_u32x4_t>((at0 ^ (S << 5)) + off);
     } else {
-      const float4 a = *reinterpret_cast<const float4*>(t + at(r, 4 * s + 2 * h));
-      const float4 b = *reinterpret_cast<const float4*>(t + at(r, 4 * s + 2 * h + 1));
-      f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
-      f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
+      const u32x4_t a = *reinterpret_cast<lds_u32x4_t>((at0 ^ (S << 6)) + off);
+      const u32x4_t b = *reinterpret_cast<lds_u32x4_t>((at0 ^ (S << 6) ^ 16) + off);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f.v[e] = __uint_as_float(a[e]);
+        f.v[4 + e] = __uint_as_float(b[e]);
+      }
     }
     return f;
   }
 
-  // Operand across the rows: column 32·blk + c of rows r0 + 4h + {0..3} and
-  // r0 + 8 + 4h + {0..3} (the order of operands formed from an accumulator).
+  // Operand across the rows: column 32·D + c of rows r0 + 4h + {0..3} and
+  // r0 + 8 + 4h + {0..3} (the order of operands formed from an accumulator),
+  // r0 a multiple of 16 in `off` (bytes).  `at0` = col_addr(tile, lane).
   // bf16: ds_read_b64_tr_b16, whose 16 lanes read a 4 x 16 block (lane i the
-  // four elements from column 4·(i mod 4) of row i/4) and get its columns.
-  __device__ static __forceinline__ Frag<IO> col_frag(const char* t, int r0, int blk, int lane) {
-    Frag<IO> f;
+  // four elements from column 4·(i mod 4) of row i/4) and get its columns;
+  // swz(r + 8) = swz(r) ^ 2 is 32 bytes.  fp32: one element a read, row by row.
+  __device__ static __forceinline__ uint32_t col_addr(uint32_t tile, int lane) {
     const int h = lane >> 5;
     if constexpr (IO == kBF16) {
-      typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_t;
-      const int i = lane & 15;
-      const int r = r0 + 4 * h + (i >> 2);
-      const int col = 32 * blk + (lane & 16) + 4 * (i & 3);
-      const int off = at(r, col >> 3) + (col & 7) * 2;
-      // swz(r + 8) = swz(r) ^ 2: two chunks, 32 bytes
-      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(t + off));
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(t + (off ^ 32) + 8 * kRow));
+      const int i = lane & 15, r = 4 * h + (i >> 2);
+      return tile + r * kRow + (((((lane & 16) >> 3) + ((i & 3) >> 1)) ^ swz(r)) << 4) + (i & 1) * 8;
+    } else {
+      const int c = lane & 31, r = 4 * h;
+      return tile + r * kRow + (((c >> 2) ^ swz(r)) << 4) + (c & 3) * 4;
+    }
+  }
+  template <int D>
+  __device__ static __forceinline__ Frag<IO> col_frag(uint32_t at0, int off) {
+    Frag<IO> f;
+    if constexpr (IO == kBF16) {
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4_t>((at0 ^ (D << 6)) + off));
+      const s16x4_t hi =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4_t>((at0 ^ (D << 6) ^ 32) + off + 8 * kRow));
       const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
       f.w = u32x4_t{a.x, a.y, b.x, b.y};
     } else {
-      const int col = 32 * blk + (lane & 31);
+      // row 4h + j + 8·(e >> 2), j < 4: swz adds 4j (chunks), and 2 for the upper four
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int r = r0 + 8 * (e >> 2) + 4 * h + (e & 3);
-        f.v[e] = *reinterpret_cast<const float*>(t + at(r, col >> 2) + (col & 3) * 4);
+        const int j = e & 3, up = e >> 2;
+        const uint32_t x = (D << 7) ^ (j << 6) ^ (up << 5);
+        f.v[e] = *reinterpret_cast<lds_float_t>((at0 ^ x) + off + (j + 8 * up) * kRow);
       }
     }
     return f;
   }
 };
+
+// An LDS pointer's byte address.
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+// f(integral constant) for 0 .. N - 1, unrolled.
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
 
 // Staging of R head rows by 256 threads: global memory to registers, then
 // registers to LDS, so that the next tile is on its way while this one is
@@ -386,17 +440,17 @@ struct RowState {
 // when it would overflow that margin (p stays ≤ 64, exact in fp32 sums, and
 // bf16 keeps its relative precision at any scale).
 template <int IO, int DH, int KB, bool MOD>
-__device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH / 16], const char* tk, const char* tv,
+__device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH / 16], uint32_t tk, uint32_t tv,
                                        int key0, int lo, int hi, bool partial, int pos, float slope2, ScoreMod mod) {
   using T = Tile<IO, DH>;
   const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h = lane >> 5;
+  const uint32_t ka = T::row_addr(tk, c, h), va = T::col_addr(tv, lane);
   f32x16_t s[KB];
 #pragma unroll
   for (int b = 0; b < KB; ++b) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < DH / 16; ++i) s[b] = mma(T::row_frag(tk, 32 * b + c, i, h), qf[i], s[b]);
+    each<DH / 16>([&](auto i) { s[b] = mma(T::template row_frag<i>(ka, 32 * b * T::kRow), qf[i], s[b]); });
   }
   float pre = mod.pre();
   if constexpr (MOD) {
@@ -454,9 +508,7 @@ __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const Frag<IO> p = frag_of<IO>(s[b], i);
-#pragma unroll
-      for (int d = 0; d < DH / 32; ++d)
-        st.o[d] = mma(T::col_frag(tv, 32 * b + 16 * i, d, lane), p, st.o[d]);
+      each<DH / 32>([&](auto d) { st.o[d] = mma(T::template col_frag<d>(va, (32 * b + 16 * i) * T::kRow), p, st.o[d]); });
     }
 }
 

@@ -39,9 +39,9 @@ template <int IO, int DH, bool MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel(FwdArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
-  extern __shared__ __attribute__((aligned(256))) char lds[];  // two buffers of a key and a value tile
+  extern __shared__ __attribute__((aligned(512))) char lds[];  // two buffers of a key and a value tile
   __shared__ int range[8];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   // Tiles from the last (under a causal mask the longest) down; the heads of a
   // tile vary fastest, key head first: consecutive workgroups go to the eight
   // XCDs in turn, so with 8 key heads (or a divisor) each XCD's L2 holds one
@@ -76,6 +76,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
   const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
   Stage<IO, DH, kKeys> sk, sv;
   const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hq] * kLog2e : 0.f;
+  settle(qf);
   RowState<DH> st;
   st.init();
   // (rows past bhi read as zeros: no row of the tile sees them)
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
     __syncthreads();
     if (key0 < whi && next > wlo) {
       const bool partial = __any(live && (lo > key0 || hi < next));
-      attend<IO, DH, kKeys / 32, MOD>(st, qf, tk, tv, key0, lo, hi, partial, i, slope2, a.mod);
+      attend<IO, DH, kKeys / 32, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, lo, hi, partial, i, slope2, a.mod);
     }
   }
   if (i >= a.mask.T || (!in_doc && !a.fill)) return;

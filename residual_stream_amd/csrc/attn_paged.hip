@@ -204,11 +204,11 @@ template <int IO, int DH, bool MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_kernel(PagedArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kFewKeys * T::kRow;
-  extern __shared__ __attribute__((aligned(256))) char lds[];  // a key and a value tile a wave; then the waves' row states
+  extern __shared__ __attribute__((aligned(512))) char lds[];  // a key and a value tile a wave; then the waves' row states
   __shared__ float wm[4][32], wl[4][32];
   __shared__ int any_bad;
   fill_rest<IO, DH>(a);
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   if (threadIdx.x == 0) any_bad = 0;
   __syncthreads();
   const int hk = blockIdx.x % a.Hk;
@@ -223,6 +223,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
   Frag<IO> qf[DH / 16];
   load_q<IO, DH>(a, r, h, qf);
   const float slope2 = MOD && a.slopes != nullptr ? a.slopes[r.hq] * kLog2e : 0.f;
+  settle(qf);
   RowState<DH> st;
   st.init();
   bool bad = false;
@@ -245,7 +246,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const bool partial = __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kFewKeys)) || key0 + kFewKeys > hi;
-    attend<IO, DH, 1, MOD>(st, qf, tk, tv, key0, r.lo, min(r.hi, hi), partial, r.pos, slope2, a.mod);
+    attend<IO, DH, 1, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, r.lo, min(r.hi, hi), partial, r.pos, slope2, a.mod);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
@@ -296,11 +297,11 @@ template <int IO, int DH, bool MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chunk_kernel(PagedArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
-  extern __shared__ __attribute__((aligned(256))) char lds[];
+  extern __shared__ __attribute__((aligned(512))) char lds[];
   __shared__ int range[8];
   __shared__ int any_bad;
   fill_rest<IO, DH>(a);
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, c = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   const int hk = blockIdx.x % a.Hk;
   int rest = blockIdx.x / a.Hk;
   const int sp = rest % a.splits;
@@ -326,6 +327,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
   Frag<IO> qf[DH / 16];
   load_q<IO, DH>(a, r, h, qf);
   const float slope2 = MOD && a.slopes != nullptr ? a.slopes[r.hq] * kLog2e : 0.f;
+  settle(qf);
   RowState<DH> st;
   st.init();
   bool bad = false;
@@ -346,7 +348,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
     __syncthreads();
     if (key0 < whi && key0 + kKeys > wlo) {
       const bool partial = __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kKeys)) || key0 + kKeys > bhi;
-      attend<IO, DH, kKeys / 32, MOD>(st, qf, tk, tv, key0, r.lo, min(r.hi, bhi), partial, r.pos, slope2, a.mod);
+      attend<IO, DH, kKeys / 32, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, r.lo, min(r.hi, bhi), partial, r.pos, slope2, a.mod);
     }
   }
   if (__any(bad) && lane == 0) any_bad = 1;
