@@ -39,20 +39,20 @@ struct BwdArgs {
 };
 
 // Score s (log 2 units) and the capping's derivative from a product x.
-template <int IO>
+template <int IO, int MOD>
 __device__ __forceinline__ void score(float x, float pre, ScoreMod mod, float slope2, float dist, float& s, float& dcap) {
   s = x * pre;
   dcap = 1.f;
-  if (mod.cap > 0.f) {
+  if constexpr ((MOD & kCapped) != 0) {
     const float t = cap_tanh<IO>(s);
     dcap = 1.f - t * t;
     s = mod.post() * t;
   }
-  s = __builtin_fmaf(-slope2, fabsf(dist), s);
+  if constexpr ((MOD & kSloped) != 0) s = __builtin_fmaf(-slope2, fabsf(dist), s);
 }
 
 // Rows: 128 of one query head a workgroup, 32 a wave; key and value tiles of 64.
-template <int IO, int DH, bool MOD>
+template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_kernel(BwdArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
   const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
   const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
   Stage<IO, DH, kKeys> sk, sv;
-  const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hq] * kLog2e : 0.f;
+  const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hq] * kLog2e : 0.f;
   settle(qf);
   settle(gf);
   asm volatile("" : "+v"(lse2), "+v"(delta));
@@ -147,12 +147,12 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
       for (int r = 0; r < 16; ++r) {
         const int k = 8 * (r >> 2) + (r & 3);
         float sc, dcap = 1.f;
-        if constexpr (MOD)
-          score<IO>(s[r], pre, a.mod, slope2, d0 - (float)k, sc, dcap);
+        if constexpr (MOD != 0)
+          score<IO, MOD>(s[r], pre, a.mod, slope2, d0 - (float)k, sc, dcap);
         else
           sc = s[r] * pre;
         float ds = exp2_fast(sc - lse2) * (dp[r] - delta);
-        if constexpr (MOD) ds *= dcap;
+        if constexpr ((MOD & kCapped) != 0) ds *= dcap;
         s[r] = ds;
       }
       if (partial) {
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
 // order.
 constexpr int kKeyThreads = 512;
 
-template <int IO, int DH, bool MOD>
+template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kQ * T::kRow;
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
     prev = buf;
     buf = buf == 2 ? 0 : buf + 1;
     if (!mine_now) continue;
-    const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hk * G + wg] * kLog2e : 0.f;
+    const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hk * G + wg] * kLog2e : 0.f;
     wrow += kQ;
     if (wrow >= bhi) {
       wrow = blo;
@@ -314,8 +314,8 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
         for (int e = 0; e < 4; ++e) {
           const int r = 4 * r4 + e;
           float sc, dcap = 1.f;
-          if constexpr (MOD)
-            score<IO>(s[r], pre, a.mod, slope2, d0 + (float)(8 * r4 + e), sc, dcap);
+          if constexpr (MOD != 0)
+            score<IO, MOD>(s[r], pre, a.mod, slope2, d0 + (float)(8 * r4 + e), sc, dcap);
           else
             sc = s[r] * pre;
           s[r] = exp2_fast(sc - lv[e]);
@@ -459,10 +459,10 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
   const dim3 rows((unsigned)((d.T + kRows - 1) / kRows * d.Hq));
   const dim3 keys((unsigned)((d.T + kKeyRows - 1) / kKeyRows * d.Hk * a.pieces));
   hipError_t err = hipErrorInvalidValue;
-  dispatch_attn(d.io, d.Dh, d.softcap > 0.f || d.slopes != nullptr, [&](auto io_, auto dh_, auto mod_) {
+  dispatch_attn(d.io, d.Dh, d.softcap, d.slopes, [&](auto io_, auto dh_, auto mod_) {
     constexpr int IO = decltype(io_)::value;
     constexpr int DH = decltype(dh_)::value;
-    constexpr bool MOD = decltype(mod_)::value;
+    constexpr int MOD = decltype(mod_)::value;
     constexpr int row = Tile<IO, DH>::kRow;
     MHC_LAUNCH((attn_bwd_rows_kernel<IO, DH, MOD>), rows, dim3(kThreads), 4 * kKeys * row, s, a);
     err = hipGetLastError();

@@ -367,6 +367,17 @@ __device__ __forceinline__ float cap_tanh(float x) {
   return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + exp2_fast(2.f * kLog2e * x));
 }
 
+// What a kernel's scores have besides the scale: bits of a template argument.
+enum Mod : int { kCapped = 1, kSloped = 2 };
+
+// The score in log 2 units of x = q·k times mod.pre(), at a signed distance.
+template <int IO, int MOD>
+__device__ __forceinline__ float modified(float x, ScoreMod mod, float slope2, float dist) {
+  if constexpr ((MOD & kCapped) != 0) x = mod.post() * cap_tanh<IO>(x);
+  if constexpr ((MOD & kSloped) != 0) x = __builtin_fmaf(-slope2, fabsf(dist), x);
+  return x;
+}
+
 // Accumulator element r's row within its 32-row block, for lane half h.
 __device__ __forceinline__ constexpr int acc_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
@@ -439,7 +450,7 @@ struct RowState {
 // The maximum is let lag by up to 2⁶: a new maximum rescales the output only
 // when it would overflow that margin (p stays ≤ 64, exact in fp32 sums, and
 // bf16 keeps its relative precision at any scale).
-template <int IO, int DH, int KB, bool MOD>
+template <int IO, int DH, int KB, int MOD>
 __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH / 16], uint32_t tk, uint32_t tv,
                                        int key0, int lo, int hi, bool partial, int pos, float slope2, ScoreMod mod) {
   using T = Tile<IO, DH>;
@@ -453,16 +464,13 @@ __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH
     each<DH / 16>([&](auto i) { s[b] = mma(T::template row_frag<i>(ka, 32 * b * T::kRow), qf[i], s[b]); });
   }
   float pre = mod.pre();
-  if constexpr (MOD) {
+  if constexpr (MOD != 0) {
     const float d0 = (float)(pos - key0 - 4 * h);
 #pragma unroll
     for (int b = 0; b < KB; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float x = s[b][r] * pre;
-        if (mod.cap > 0.f) x = mod.post() * cap_tanh<IO>(x);
-        s[b][r] = __builtin_fmaf(-slope2, fabsf(d0 - (float)(32 * b + 8 * (r >> 2) + (r & 3))), x);
-      }
+      for (int r = 0; r < 16; ++r)
+        s[b][r] = modified<IO, MOD>(s[b][r] * pre, mod, slope2, d0 - (float)(32 * b + 8 * (r >> 2) + (r & 3)));
     pre = 1.f;
   }
   if (partial) {
@@ -514,16 +522,19 @@ __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH
 
 }  // namespace attn
 
-// Calls f(io, head size, modified scores) as integral constants for the
+// Calls f(io, head size, score modification) as integral constants for the
 // supported kinds.
 template <typename F>
-__host__ bool dispatch_attn(int io, int dh, bool mod, F&& f) {
+__host__ bool dispatch_attn(int io, int dh, float cap, const float* slopes, F&& f) {
+  const int mod = (cap > 0.f ? attn::kCapped : 0) | (slopes != nullptr ? attn::kSloped : 0);
   return dispatch_io(io, [&](auto io_) {
     auto with_dh = [&](auto dh_) {
-      if (mod)
-        f(io_, dh_, std::true_type{});
-      else
-        f(io_, dh_, std::false_type{});
+      switch (mod) {
+        case 0: f(io_, dh_, std::integral_constant<int, 0>{}); break;
+        case 1: f(io_, dh_, std::integral_constant<int, 1>{}); break;
+        case 2: f(io_, dh_, std::integral_constant<int, 2>{}); break;
+        default: f(io_, dh_, std::integral_constant<int, 3>{}); break;
+      }
     };
     if (dh == 64)
       with_dh(std::integral_constant<int, 64>{});

@@ -35,7 +35,7 @@ struct FwdArgs {
   int64_t ldq, ldk, ldv, ldo;
 };
 
-template <int IO, int DH, bool MOD>
+template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel(FwdArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
   const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
   const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
   Stage<IO, DH, kKeys> sk, sv;
-  const float slope2 = MOD && a.slopes != nullptr ? a.slopes[hq] * kLog2e : 0.f;
+  const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hq] * kLog2e : 0.f;
   settle(qf);
   RowState<DH> st;
   st.init();
@@ -149,10 +149,10 @@ hipError_t launch_attn(const mhc_attn_desc& d, const void* q, const void* k, con
   a.ldo = d.ldo;
   const dim3 grid((unsigned)((d.T + kRows - 1) / kRows * d.Hq));
   hipError_t err = hipErrorInvalidValue;
-  dispatch_attn(d.io, d.Dh, d.softcap > 0.f || d.slopes != nullptr, [&](auto io_, auto dh_, auto mod_) {
+  dispatch_attn(d.io, d.Dh, d.softcap, d.slopes, [&](auto io_, auto dh_, auto mod_) {
     constexpr int IO = decltype(io_)::value;
     constexpr int DH = decltype(dh_)::value;
-    constexpr bool MOD = decltype(mod_)::value;
+    constexpr int MOD = decltype(mod_)::value;
     constexpr int lds = 4 * kKeys * Tile<IO, DH>::kRow;
     MHC_LAUNCH((attn_fwd_kernel<IO, DH, MOD>), grid, dim3(kThreads), lds, s, a);
     err = hipGetLastError();

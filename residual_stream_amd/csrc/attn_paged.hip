@@ -107,10 +107,10 @@ __device__ __forceinline__ Row row_of(const PagedArgs& a, int s, const Seq& q, i
   return r;
 }
 
-// Staging of R cache rows by NT threads: as Stage, with each row's place
-// looked up in the page table one tile ahead of its load.  Rows past `last`
-// re-read it (they are masked, and what is read is finite wherever the last
-// row's keys and values are).
+// Staging of R cache rows by NT threads: as Stage, with each row's entry of
+// the page table read one tile ahead of its load (and not looked at before, so
+// that nothing waits for it).  Rows past `last` re-read it (they are masked,
+// and what is read is finite wherever the last row's keys and values are).
 template <int IO, int DH, int R, int NT>
 struct PagedStage {
   using T = Tile<IO, DH>;
@@ -118,29 +118,30 @@ struct PagedStage {
   static constexpr int kStep = NT / T::kChunks;
   static_assert(R * T::kChunks % NT == 0 && NT % T::kChunks == 0, "whole passes");
   u32x4_t k[kN], v[kN];
-  int place[kN];
+  int entry[kN];
 
-  __device__ __forceinline__ void lookup(const PagedArgs& a, const int32_t* table, int thread, int row0, int last,
-                                         bool& bad) {
+  __device__ __forceinline__ void lookup(const PagedArgs& a, const int32_t* table, int thread, int row0, int last) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) entry[n] = table[a.by_page(min(row0 + thread / T::kChunks + n * kStep, last))];
+  }
+  __device__ __forceinline__ void load(const PagedArgs& a, int hk, int thread, int row0, int last, bool& bad) {
+    const int64_t row = (int64_t)a.Hk * T::kRow;
+    const int64_t in = (int64_t)hk * T::kRow + (thread % T::kChunks) * 16;
+    int64_t at[kN];
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       const int r = min(row0 + thread / T::kChunks + n * kStep, last);
-      const int p = a.by_page(r);
-      int e = table[p];
+      int e = entry[n];
       if ((unsigned)e >= (unsigned)a.num_pages) {
         bad = true;
         e = 0;
       }
-      place[n] = e * a.page_size + (r - p * a.page_size);
+      at[n] = (e * a.page_size + (r - a.by_page(r) * a.page_size)) * row + in;
     }
-  }
-  __device__ __forceinline__ void load(const PagedArgs& a, int hk, int thread) {
-    const int64_t row = (int64_t)a.Hk * T::kRow;
-    const int64_t in = (int64_t)hk * T::kRow + (thread % T::kChunks) * 16;
 #pragma unroll
-    for (int n = 0; n < kN; ++n) k[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.kc) + place[n] * row + in);
+    for (int n = 0; n < kN; ++n) k[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.kc) + at[n]);
 #pragma unroll
-    for (int n = 0; n < kN; ++n) v[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.vc) + place[n] * row + in);
+    for (int n = 0; n < kN; ++n) v[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.vc) + at[n]);
   }
   __device__ __forceinline__ void store(char* tk, char* tv, int thread) const {
 #pragma unroll
@@ -200,7 +201,7 @@ __device__ __forceinline__ void split_range(int splits, int sp, int step, int& l
 
 // Few rows: one tile of up to 32 packed rows, which every wave holds; the
 // waves take the key tiles of 32 in turn and join their row states in LDS.
-template <int IO, int DH, bool MOD>
+template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_kernel(PagedArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kFewKeys * T::kRow;
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
 
   Frag<IO> qf[DH / 16];
   load_q<IO, DH>(a, r, h, qf);
-  const float slope2 = MOD && a.slopes != nullptr ? a.slopes[r.hq] * kLog2e : 0.f;
+  const float slope2 = (MOD & kSloped) != 0 ? a.slopes[r.hq] * kLog2e : 0.f;
   settle(qf);
   RowState<DH> st;
   st.init();
@@ -234,14 +235,14 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
   int key0 = lo + wave * kFewKeys;
   constexpr int kAll = 4 * kFewKeys;
   if (key0 < hi) {
-    sg.lookup(a, table, lane, key0, hi - 1, bad);
-    sg.load(a, hk, lane);
-    if (key0 + kAll < hi) sg.lookup(a, table, lane, key0 + kAll, hi - 1, bad);
+    sg.lookup(a, table, lane, key0, hi - 1);
+    sg.load(a, hk, lane, key0, hi - 1, bad);
+    if (key0 + kAll < hi) sg.lookup(a, table, lane, key0 + kAll, hi - 1);
   }
   for (; key0 < hi; key0 += kAll) {
     sg.store(tk, tv, lane);
-    if (key0 + kAll < hi) sg.load(a, hk, lane);
-    if (key0 + 2 * kAll < hi) sg.lookup(a, table, lane, key0 + 2 * kAll, hi - 1, bad);
+    if (key0 + kAll < hi) sg.load(a, hk, lane, key0 + kAll, hi - 1, bad);
+    if (key0 + 2 * kAll < hi) sg.lookup(a, table, lane, key0 + 2 * kAll, hi - 1);
     // the wave's own LDS: its writes come before its reads
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -293,7 +294,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
 }
 
 // Many rows: 128 packed rows of one sequence and key head, 32 a wave.
-template <int IO, int DH, bool MOD>
+template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chunk_kernel(PagedArgs a) {
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
 
   Frag<IO> qf[DH / 16];
   load_q<IO, DH>(a, r, h, qf);
-  const float slope2 = MOD && a.slopes != nullptr ? a.slopes[r.hq] * kLog2e : 0.f;
+  const float slope2 = (MOD & kSloped) != 0 ? a.slopes[r.hq] * kLog2e : 0.f;
   settle(qf);
   RowState<DH> st;
   st.init();
@@ -334,17 +335,17 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
   PagedStage<IO, DH, kKeys, kThreads> sg;
   const int32_t* table = a.pages + (int64_t)s * a.max_pages;
   if (blo < bhi) {
-    sg.lookup(a, table, threadIdx.x, blo, bhi - 1, bad);
-    sg.load(a, hk, threadIdx.x);
-    if (blo + kKeys < bhi) sg.lookup(a, table, threadIdx.x, blo + kKeys, bhi - 1, bad);
+    sg.lookup(a, table, threadIdx.x, blo, bhi - 1);
+    sg.load(a, hk, threadIdx.x, blo, bhi - 1, bad);
+    if (blo + kKeys < bhi) sg.lookup(a, table, threadIdx.x, blo + kKeys, bhi - 1);
   }
   int buf = 0;
   for (int key0 = blo; key0 < bhi; key0 += kKeys, buf ^= 1) {
     char* tk = lds + buf * 2 * kTile;
     char* tv = tk + kTile;
     sg.store(tk, tv, threadIdx.x);
-    if (key0 + kKeys < bhi) sg.load(a, hk, threadIdx.x);
-    if (key0 + 2 * kKeys < bhi) sg.lookup(a, table, threadIdx.x, key0 + 2 * kKeys, bhi - 1, bad);
+    if (key0 + kKeys < bhi) sg.load(a, hk, threadIdx.x, key0 + kKeys, bhi - 1, bad);
+    if (key0 + 2 * kKeys < bhi) sg.lookup(a, table, threadIdx.x, key0 + 2 * kKeys, bhi - 1);
     __syncthreads();
     if (key0 < whi && key0 + kKeys > wlo) {
       const bool partial = __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kKeys)) || key0 + kKeys > bhi;
@@ -455,10 +456,10 @@ hipError_t launch_attn_paged(const mhc_paged_desc& d, const void* q, const void*
   const bool few = few_rows(d);
   const dim3 grid((unsigned)((int64_t)d.n_seqs * d.Hk * a.tiles * a.splits));
   hipError_t err = hipErrorInvalidValue;
-  dispatch_attn(d.io, d.Dh, d.softcap > 0.f || d.slopes != nullptr, [&](auto io_, auto dh_, auto mod_) {
+  dispatch_attn(d.io, d.Dh, d.softcap, d.slopes, [&](auto io_, auto dh_, auto mod_) {
     constexpr int IO = decltype(io_)::value;
     constexpr int DH = decltype(dh_)::value;
-    constexpr bool MOD = decltype(mod_)::value;
+    constexpr int MOD = decltype(mod_)::value;
     constexpr int row = Tile<IO, DH>::kRow;
     // few: four waves' tiles, or their fp32 row states
     constexpr int few_lds = 4 * 2 * kFewKeys * row > 4 * 32 * DH * 4 ? 4 * 2 * kFewKeys * row : 4 * 32 * DH * 4;
