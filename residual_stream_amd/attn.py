@@ -11,6 +11,9 @@ any token stride that is a multiple of 8 elements, so q, k and v may be views
 of one projection's output (``qkv[:, :Hq*Dh].unflatten(1, (Hq, Dh))``), and
 gradients passed in ``out`` views of its gradient.  Query head h reads key
 head ``h // (Hq // Hk)``.
+
+A decode step makes these calls once a layer, so the checks are kept short:
+each takes one look at a tensor and words its refusal only when there is one.
 """
 
 from __future__ import annotations
@@ -20,52 +23,97 @@ import ctypes
 import torch
 
 from . import mhc
-from .mhc import MhcAttnDesc, MhcPagedDesc, MhcRopeDesc, _check, _expect, _io_of, _stream, _workspace, _ws_bytes, load
+from .mhc import MhcAttnDesc, MhcPagedDesc, MhcRopeDesc, _check, _workspace, _ws_bytes, load
+
+_IO = {torch.float32: mhc.MHC_F32, torch.bfloat16: mhc.MHC_BF16}
+_ref = ctypes.byref
 
 
-def _head_tensor(name, t, shape=None, dtype=None, device=None):
-    """Checks one [T, H, Dh] tensor; returns its token stride in elements."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
-        raise ValueError(f"{name} must be a [T, H, Dh] tensor")
+def _refuse(name, t, shape, dtype, dev):
+    """Words what is wrong with one tensor argument."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise RuntimeError("the mHC kernels need GPU tensors (no CPU path)")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"{name}'s heads must be contiguous (only the token stride is free)")
-    ld = t.stride(0) if T > 1 else H * D
-    if ld < H * D or ld % 8:
-        raise ValueError(f"{name}'s token stride {ld} must be a multiple of 8 and at least {H * D}")
-    if t.data_ptr() % 16:
-        raise ValueError(f"{name} must be 16-byte aligned")
+    if t.dim() == 3 and not t.is_contiguous():
+        raise ValueError(f"{name}'s heads must be contiguous, its token stride a multiple of 8 and at least H·Dh "
+                         f"(strides {t.stride()})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _heads(name, t, shape, dtype, dev):
+    """Token stride in elements of a [T, H, Dh] tensor."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.shape != shape or t.dtype != dtype:
+        _refuse(name, t, shape, dtype, dev)
+    T, H, D = shape
+    ld, sh, sd = t.stride()
+    if T <= 1:
+        ld = H * D
+    if (sh != D and H > 1) or sd != 1 or ld < H * D or ld & 7 or (t.data_ptr() & 15 and T):
+        _refuse(name, t, shape, dtype, dev)
     return ld
 
 
+def _vec(name, t, shape, dtype, dev):
+    """Address of a contiguous tensor, None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.shape != shape or t.dtype != dtype \
+            or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _need(name, t):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
+
+
 def _queries(q):
-    """(T, Hq, Dh, dtype, device) of the query tensor."""
-    _head_tensor("q", q)
-    _io_of(q)
-    if q.device.index != torch.cuda.current_device():
+    """(shape, dtype, io, device index) of the query tensor."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, H, Dh] tensor")
+    if not q.is_cuda:
+        raise RuntimeError("the mHC kernels need GPU tensors (no CPU path)")
+    io = _IO.get(q.dtype)
+    if io is None:
+        raise TypeError(f"I/O tensors must be float32 or bfloat16, got {q.dtype}")
+    dev = q.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"q is on {q.device}; make it the current device first")
-    return (*q.shape, q.dtype, q.device)
+    return q.shape, q.dtype, io, dev
 
 
-def _grouped(Hq, Hk):
-    if Hk < 1 or Hq % Hk:
-        raise ValueError(f"{Hq} query heads cannot share {Hk} key heads evenly")
+def _key_shape(k, q_shape):
+    """Shape that k and v must have: their own number of heads, which the query heads share evenly."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [T, H, Dh] tensor")
+    Hk = k.shape[1]
+    if Hk < 1 or q_shape[1] % Hk:
+        raise ValueError(f"{q_shape[1]} query heads cannot share {Hk} key heads evenly")
+    return torch.Size((q_shape[0], Hk, q_shape[2]))
 
 
-def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _stream_of(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _vec(name, t, n, dtype, device, optional=True):
-    _expect(name, t, (n,), dtype, device, optional=optional)
+def _scratch(need, workspace, device):
+    """(address, bytes, tensor) of a workspace: the caller's, or one for this call."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _workspace(need, device)
+    return workspace.data_ptr(), _ws_bytes(workspace), workspace
 
 
 def rope_freqs(rotated: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -73,20 +121,21 @@ def rope_freqs(rotated: int, base: float = 10000.0, device="cuda") -> torch.Tens
     return base ** (-torch.arange(0, rotated, 2, dtype=torch.float64, device=device) / rotated)
 
 
-def _rope_desc(q, k, positions, freqs, q_weight, k_weight, eps, interleaved):
-    T, Hq, Dh, io, dv = _queries(q)
-    Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
-    ldk = _head_tensor("k", k, (T, Hk, Dh), io, dv)
-    _grouped(Hq, Hk)
-    _vec("positions", positions, T, torch.int32, dv, optional=False)
+def _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved):
+    """(descriptor, key shape, addresses of q, k, positions, freqs and weights, dtype, device) of a rope call."""
+    shape, dtype, io, dev = _queries(q)
+    T, Hq, Dh = shape
+    ks = _key_shape(k, shape)
+    Hk = ks[1]
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise ValueError("freqs must be a [R/2] tensor")
-    _vec("freqs", freqs, freqs.shape[0], torch.float64, dv, optional=False)
-    _vec("q_weight", q_weight, Dh, torch.float32, dv)
-    _vec("k_weight", k_weight, Dh, torch.float32, dv)
-    return MhcRopeDesc(T=T, Hq=Hq, Hk=Hk, Dh=Dh, R=2 * freqs.shape[0], io=_io_of(q), interleaved=int(bool(interleaved)),
-                       eps=float(eps), ldq=_head_tensor("q", q), ldk=ldk, ldv=Hk * Dh, ldq_out=Hq * Dh, ldk_out=Hk * Dh,
-                       ld_dq=Hq * Dh, ld_dk=Hk * Dh)
+    half = freqs.shape[0]
+    d = MhcRopeDesc(T, Hq, Hk, Dh, 2 * half, io, 1 if interleaved else 0, eps, 0, _heads("q", q, shape, dtype, dev),
+                    _heads("k", k, ks, dtype, dev), Hk * Dh, Hq * Dh, Hk * Dh, Hq * Dh, Hk * Dh)
+    at = (q.data_ptr(), k.data_ptr(), _vec("positions", _need("positions", positions), (T,), torch.int32, dev),
+          _vec("freqs", freqs, (half,), torch.float64, dev), _vec("q_weight", q_weight, (Dh,), torch.float32, dev),
+          _vec("k_weight", k_weight, (Dh,), torch.float32, dev))
+    return d, ks, at, dtype, dev
 
 
 def mhc_qk_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None,
@@ -97,14 +146,13 @@ def mhc_qk_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-
 
     Returns (q_out[T,Hq,Dh], k_out[T,Hk,Dh])."""
     lib = load()
-    d = _rope_desc(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
+    d, ks, at, dtype, dev = _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
     if out is None:
-        out = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        out = (torch.empty(q.shape, dtype=dtype, device=q.device), torch.empty(ks, dtype=dtype, device=q.device))
     qo, ko = out
-    d.ldq_out = _head_tensor("q_out", qo, q.shape, q.dtype, q.device)
-    d.ldk_out = _head_tensor("k_out", ko, k.shape, q.dtype, q.device)
-    _check(lib.mhc_qk_rope(ctypes.byref(d), _p(q), _p(k), _p(positions), _p(freqs), _p(q_weight), _p(k_weight), _p(qo),
-                           _p(ko), _stream(stream)), "mhc_qk_rope")
+    d.ldq_out = _heads("q_out", qo, q.shape, dtype, dev)
+    d.ldk_out = _heads("k_out", ko, ks, dtype, dev)
+    _check(lib.mhc_qk_rope(_ref(d), *at, qo.data_ptr(), ko.data_ptr(), _stream_of(stream, dev)), "mhc_qk_rope")
     return out
 
 
@@ -114,38 +162,34 @@ def mhc_qk_rope_bwd(dq_out, dk_out, q, k, positions, freqs, *, q_weight=None, k_
     dq_weight[Dh] or None, dk_weight[Dh] or None), the weights' gradients in
     fp32 summed over tokens and heads."""
     lib = load()
-    d = _rope_desc(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
-    dv = q.device
-    d.ldq_out = _head_tensor("dq_out", dq_out, q.shape, q.dtype, dv)
-    d.ldk_out = _head_tensor("dk_out", dk_out, k.shape, q.dtype, dv)
+    d, ks, at, dtype, dev = _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
+    d.ldq_out = _heads("dq_out", dq_out, q.shape, dtype, dev)
+    d.ldk_out = _heads("dk_out", dk_out, ks, dtype, dev)
     if out is None:
-        out = tuple(torch.empty(t.shape, dtype=t.dtype, device=dv) for t in (q, k)) + tuple(
-            None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
+        out = (torch.empty(q.shape, dtype=dtype, device=q.device), torch.empty(ks, dtype=dtype, device=q.device),
+               None if q_weight is None else torch.empty_like(q_weight),
+               None if k_weight is None else torch.empty_like(k_weight))
     dq, dk, dqw, dkw = out
-    d.ld_dq = _head_tensor("dq", dq, q.shape, q.dtype, dv)
-    d.ld_dk = _head_tensor("dk", dk, k.shape, q.dtype, dv)
+    d.ld_dq = _heads("dq", dq, q.shape, dtype, dev)
+    d.ld_dk = _heads("dk", dk, ks, dtype, dev)
     for name, g, w in (("dq_weight", dqw, q_weight), ("dk_weight", dkw, k_weight)):
         if g is not None and w is None:
             raise ValueError(f"{name} without the weight itself")
-        _vec(name, g, q.shape[2], torch.float32, dv)
-    need = lib.mhc_qk_rope_bwd_workspace_bytes(ctypes.byref(d))
-    if workspace is None and need:
-        workspace = _workspace(need, dv)
-    nbytes = _ws_bytes(workspace)
-    _check(lib.mhc_qk_rope_bwd(ctypes.byref(d), _p(dq_out), _p(dk_out), _p(q), _p(k), _p(positions), _p(freqs),
-                               _p(q_weight), _p(k_weight), _p(dq), _p(dk), _p(dqw), _p(dkw), _p(workspace), nbytes,
-                               _stream(stream)), "mhc_qk_rope_bwd")
+    row = (q.shape[2],)
+    grads = (_vec("dq_weight", dqw, row, torch.float32, dev), _vec("dk_weight", dkw, row, torch.float32, dev))
+    ws, nbytes, _keep = _scratch(lib.mhc_qk_rope_bwd_workspace_bytes(_ref(d)), workspace, q.device)
+    _check(lib.mhc_qk_rope_bwd(_ref(d), dq_out.data_ptr(), dk_out.data_ptr(), *at, dq.data_ptr(), dk.data_ptr(), *grads,
+                               ws, nbytes, _stream_of(stream, dev)), "mhc_qk_rope_bwd")
     return out
 
 
-def _cache(k_cache, v_cache, Hk, Dh, dtype, device):
-    """(pages, page size) of the two caches [pages, page_size, Hk, Dh]."""
+def _cache(k_cache, v_cache, Hk, Dh, dtype, dev):
+    """(pages, page size) of the two caches [pages, page_size, Hk, Dh], and their addresses."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [pages, page_size, Hk, Dh] tensor")
     pages, size = k_cache.shape[:2]
-    _expect("k_cache", k_cache, (pages, size, Hk, Dh), dtype, device)
-    _expect("v_cache", v_cache, (pages, size, Hk, Dh), dtype, device)
-    return pages, size
+    shape = (pages, size, Hk, Dh)
+    return pages, size, _vec("k_cache", k_cache, shape, dtype, dev), _vec("v_cache", _need("v_cache", v_cache), shape, dtype, dev)
 
 
 def mhc_qk_rope_cache(q, k, v, positions, freqs, k_cache, v_cache, slots, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -156,45 +200,41 @@ def mhc_qk_rope_cache(q, k, v, positions, freqs, k_cache, v_cache, slots, *, q_w
     padded token) writes nothing.  Slots of one call must differ.  Returns
     q_out[T,Hq,Dh]."""
     lib = load()
-    d = _rope_desc(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
-    dv = q.device
-    d.ldv = _head_tensor("v", v, k.shape, q.dtype, dv)
-    pages, size = _cache(k_cache, v_cache, d.Hk, d.Dh, q.dtype, dv)
-    _vec("slots", slots, d.T, torch.int64, dv, optional=False)
+    d, ks, at, dtype, dev = _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
+    d.ldv = _heads("v", v, ks, dtype, dev)
+    pages, size, kc, vc = _cache(k_cache, v_cache, ks[1], ks[2], dtype, dev)
+    to = _vec("slots", _need("slots", slots), (ks[0],), torch.int64, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dv)
-    d.ldq_out = _head_tensor("q_out", out, q.shape, q.dtype, dv)
-    _check(lib.mhc_qk_rope_cache(ctypes.byref(d), _p(q), _p(k), _p(v), _p(positions), _p(freqs), _p(q_weight),
-                                 _p(k_weight), _p(out), _p(k_cache), _p(v_cache), _p(slots), pages * size,
-                                 _stream(stream)), "mhc_qk_rope_cache")
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    d.ldq_out = _heads("q_out", out, q.shape, dtype, dev)
+    _check(lib.mhc_qk_rope_cache(_ref(d), at[0], at[1], v.data_ptr(), *at[2:], out.data_ptr(), kc, vc, to, pages * size,
+                                 _stream_of(stream, dev)), "mhc_qk_rope_cache")
     return out
 
 
-def _constant(name, t):
-    if t is not None and isinstance(t, torch.Tensor) and t.requires_grad:
-        raise ValueError(f"{name} takes no gradient: detach it")
+def _slopes(slopes, Hq, dev):
+    if slopes is not None and isinstance(slopes, torch.Tensor) and slopes.requires_grad:
+        raise ValueError("slopes takes no gradient: detach it")
+    return _vec("slopes", slopes, (Hq,), torch.float32, dev)
 
 
-def _attn_desc(q, k, v, docs, causal, prefix, window, softcap, slopes, scale):
-    T, Hq, Dh, io, dv = _queries(q)
-    Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
-    ldk = _head_tensor("k", k, (T, Hk, Dh), io, dv)
-    ldv = _head_tensor("v", v, (T, Hk, Dh), io, dv)
-    _grouped(Hq, Hk)
+def _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale):
+    """(descriptor, key shape, addresses of q, k, v, dtype, device) of a dense attention call."""
+    shape, dtype, io, dev = _queries(q)
+    T, Hq, Dh = shape
+    ks = _key_shape(k, shape)
+    Hk = ks[1]
     n = 1
     if docs is not None:
         if not isinstance(docs, torch.Tensor) or docs.dim() != 1 or docs.shape[0] < 2:
             raise ValueError("docs must be a [n_docs + 1] tensor of row offsets")
         n = docs.shape[0] - 1
-        _vec("docs", docs, n + 1, torch.int32, dv)
-    _vec("prefix", prefix, n, torch.int32, dv)
-    _vec("slopes", slopes, Hq, torch.float32, dv)
-    _constant("slopes", slopes)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return MhcAttnDesc(T=T, Hq=Hq, Hk=Hk, Dh=Dh, io=_io_of(q), n_docs=n, causal=int(bool(causal)), window=int(window),
-                       fill_outside=0, scale=float(Dh ** -0.5 if scale is None else scale), softcap=float(softcap),
-                       docs=ptr(docs), prefix=ptr(prefix), slopes=ptr(slopes), ldq=_head_tensor("q", q), ldk=ldk, ldv=ldv,
-                       ldo=Hq * Dh, ld_do=Hq * Dh, ld_dq=Hq * Dh, ld_dk=Hk * Dh, ld_dv=Hk * Dh)
+    nq, nk = Hq * Dh, Hk * Dh
+    d = MhcAttnDesc(T, Hq, Hk, Dh, io, n, 1 if causal else 0, window, 0, Dh ** -0.5 if scale is None else scale, softcap,
+                    _vec("docs", docs, (n + 1,), torch.int32, dev), _vec("prefix", prefix, (n,), torch.int32, dev),
+                    _slopes(slopes, Hq, dev), _heads("q", q, shape, dtype, dev), _heads("k", k, ks, dtype, dev),
+                    _heads("v", v, ks, dtype, dev), nq, nq, nq, nk, nk)
+    return d, ks, (q.data_ptr(), k.data_ptr(), v.data_ptr()), dtype, dev
 
 
 def saved_floats(T: int, Hq: int, Dh: int, io: int) -> int:
@@ -205,12 +245,10 @@ def saved_floats(T: int, Hq: int, Dh: int, io: int) -> int:
     return lse + (T * Hq * Dh // 4 if io == mhc.MHC_BF16 else 0)
 
 
-def _saved(name, saved, d, device):
-    """(lse, o_rest) pointers within the saved tensor."""
-    n = saved_floats(d.T, d.Hq, d.Dh, d.io)
-    _expect(name, saved, (n,), torch.float32, device)
-    lse = saved.data_ptr()
-    return ctypes.c_void_p(lse), (ctypes.c_void_p(lse + (-(-d.Hq * d.T // 4) * 16)) if d.io == mhc.MHC_BF16 else None)
+def _saved(saved, d, dev):
+    """Addresses of the log-sum-exps and of o's further bits within the saved tensor."""
+    lse = _vec("saved", _need("saved", saved), (saved_floats(d.T, d.Hq, d.Dh, d.io),), torch.float32, dev)
+    return lse, (lse + (-(-d.Hq * d.T // 4) * 16) if d.io == mhc.MHC_BF16 else None)
 
 
 def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=0.0, slopes=None, scale=None, out=None,
@@ -228,15 +266,15 @@ def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=
     log-sum-exps [Hq, T].  Rows of no document come out as zeros (lse -inf); in
     tensors passed as ``out=(o, saved or None)`` they are left as they were."""
     lib = load()
-    d = _attn_desc(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
+    d, _ks, at, dtype, dev = _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
     if out is None:
         d.fill_outside = 1
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+        out = (torch.empty(q.shape, dtype=dtype, device=q.device),
                torch.empty(saved_floats(d.T, d.Hq, d.Dh, d.io), dtype=torch.float32, device=q.device))
     o, saved = out
-    d.ldo = _head_tensor("o", o, q.shape, q.dtype, q.device)
-    lse, rest = (None, None) if saved is None else _saved("saved", saved, d, q.device)
-    _check(lib.mhc_attn(ctypes.byref(d), _p(q), _p(k), _p(v), _p(o), lse, rest, _stream(stream)), "mhc_attn")
+    d.ldo = _heads("o", o, q.shape, dtype, dev)
+    lse, rest = (None, None) if saved is None else _saved(saved, d, dev)
+    _check(lib.mhc_attn(_ref(d), *at, o.data_ptr(), lse, rest, _stream_of(stream, dev)), "mhc_attn")
     return out
 
 
@@ -247,22 +285,20 @@ def mhc_attn_bwd(do, q, k, v, o, saved, *, docs=None, causal=True, prefix=None, 
     no document get zeros, or are left as they were in tensors passed as
     ``out``."""
     lib = load()
-    d = _attn_desc(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
-    dv = q.device
-    d.ld_do = _head_tensor("do", do, q.shape, q.dtype, dv)
-    d.ldo = _head_tensor("o", o, q.shape, q.dtype, dv)
-    lse, rest = _saved("saved", saved, d, dv)
+    d, ks, at, dtype, dev = _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
+    d.ld_do = _heads("do", do, q.shape, dtype, dev)
+    d.ldo = _heads("o", o, q.shape, dtype, dev)
+    lse, rest = _saved(saved, d, dev)
     if out is None:
         d.fill_outside = 1
-        out = tuple(torch.empty(t.shape, dtype=t.dtype, device=dv) for t in (q, k, v))
-    d.ld_dq, d.ld_dk, d.ld_dv = (_head_tensor(n, g, t.shape, q.dtype, dv)
-                                 for n, g, t in zip(("dq", "dk", "dv"), out, (q, k, v)))
-    need = lib.mhc_attn_bwd_workspace_bytes(ctypes.byref(d))
-    if workspace is None and need:
-        workspace = _workspace(need, dv)
-    nbytes = _ws_bytes(workspace)
-    _check(lib.mhc_attn_bwd(ctypes.byref(d), _p(do), _p(q), _p(k), _p(v), _p(o), lse, rest, *(_p(g) for g in out),
-                            _p(workspace), nbytes, _stream(stream)), "mhc_attn_bwd")
+        out = tuple(torch.empty(s, dtype=dtype, device=q.device) for s in (q.shape, ks, ks))
+    dq, dk, dv = out
+    d.ld_dq = _heads("dq", dq, q.shape, dtype, dev)
+    d.ld_dk = _heads("dk", dk, ks, dtype, dev)
+    d.ld_dv = _heads("dv", dv, ks, dtype, dev)
+    ws, nbytes, _keep = _scratch(lib.mhc_attn_bwd_workspace_bytes(_ref(d)), workspace, q.device)
+    _check(lib.mhc_attn_bwd(_ref(d), do.data_ptr(), *at, o.data_ptr(), lse, rest, dq.data_ptr(), dk.data_ptr(),
+                            dv.data_ptr(), ws, nbytes, _stream_of(stream, dev)), "mhc_attn_bwd")
     return out
 
 
@@ -282,21 +318,17 @@ def mhc_attn_paged(q, k_cache, v_cache, pages, kv_lens, *, cu_q=None, max_q=None
     a page outside the cache NaN; rows of no sequence get zeros, or are left as
     they were in a tensor passed as ``out``."""
     lib = load()
-    T, Hq, Dh, io, dv = _queries(q)
+    shape, dtype, io, dev = _queries(q)
+    T, Hq, Dh = shape
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [pages, page_size, Hk, Dh] tensor")
     Hk = k_cache.shape[2]
-    _grouped(Hq, Hk)
-    num, size = _cache(k_cache, v_cache, Hk, Dh, io, dv)
+    if Hk < 1 or Hq % Hk:
+        raise ValueError(f"{Hq} query heads cannot share {Hk} key heads evenly")
+    num, size, kc, vc = _cache(k_cache, v_cache, Hk, Dh, dtype, dev)
     if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
         raise ValueError("pages must be a [n, max_pages] tensor")
     n, width = pages.shape
-    _expect("pages", pages, (n, width), torch.int32, dv)
-    _vec("kv_lens", kv_lens, n, torch.int32, dv, optional=False)
-    _vec("cu_q", cu_q, n + 1, torch.int32, dv)
-    _vec("prefix", prefix, n, torch.int32, dv)
-    _vec("slopes", slopes, Hq, torch.float32, dv)
-    _constant("slopes", slopes)
     if cu_q is None:
         if n > T:
             raise ValueError(f"{n} sequences but {T} rows (pass cu_q for chunks)")
@@ -305,19 +337,15 @@ def mhc_attn_paged(q, k_cache, v_cache, pages, kv_lens, *, cu_q=None, max_q=None
         max_q = 1
     elif max_q is None:
         max_q = max(T, 1)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    d = MhcPagedDesc(T=T, n_seqs=n, max_q=int(max_q), Hq=Hq, Hk=Hk, Dh=Dh, io=_io_of(q), window=int(window),
-                     page_size=size, max_pages=width, fill_outside=int(out is None), num_pages=num,
-                     scale=float(Dh ** -0.5 if scale is None else scale), softcap=float(softcap), cu_q=ptr(cu_q),
-                     kv_lens=ptr(kv_lens), pages=ptr(pages), prefix=ptr(prefix), slopes=ptr(slopes),
-                     ldq=_head_tensor("q", q), ldo=Hq * Dh)
+    d = MhcPagedDesc(T, n, max_q, Hq, Hk, Dh, io, window, size, width, 1 if out is None else 0, num,
+                     Dh ** -0.5 if scale is None else scale, softcap, _vec("cu_q", cu_q, (n + 1,), torch.int32, dev),
+                     _vec("kv_lens", _need("kv_lens", kv_lens), (n,), torch.int32, dev),
+                     _vec("pages", pages, (n, width), torch.int32, dev), _vec("prefix", prefix, (n,), torch.int32, dev),
+                     _slopes(slopes, Hq, dev), _heads("q", q, shape, dtype, dev), Hq * Dh)
     if out is None:
-        out = torch.empty(q.shape, dtype=io, device=dv) if n else torch.zeros(q.shape, dtype=io, device=dv)
-    d.ldo = _head_tensor("o", out, q.shape, io, dv)
-    need = lib.mhc_attn_paged_workspace_bytes(ctypes.byref(d))
-    if workspace is None and need:
-        workspace = _workspace(need, dv)
-    nbytes = _ws_bytes(workspace)
-    _check(lib.mhc_attn_paged(ctypes.byref(d), _p(q), _p(k_cache), _p(v_cache), _p(out), _p(workspace), nbytes,
-                              _stream(stream)), "mhc_attn_paged")
+        out = (torch.empty if n else torch.zeros)(shape, dtype=dtype, device=q.device)
+    d.ldo = _heads("o", out, shape, dtype, dev)
+    ws, nbytes, _keep = _scratch(lib.mhc_attn_paged_workspace_bytes(_ref(d)), workspace, q.device)
+    _check(lib.mhc_attn_paged(_ref(d), q.data_ptr(), kc, vc, out.data_ptr(), ws, nbytes, _stream_of(stream, dev)),
+           "mhc_attn_paged")
     return out

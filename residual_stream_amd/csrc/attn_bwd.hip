@@ -18,6 +18,7 @@ namespace mhc {
 using namespace attn;
 
 attn::DocMask doc_mask(const mhc_attn_desc& d);
+bool attn_short(const mhc_attn_desc& d);
 
 namespace {
 
@@ -51,6 +52,86 @@ __device__ __forceinline__ void score(float x, float pre, ScoreMod mod, float sl
   if constexpr ((MOD & kSloped) != 0) s = __builtin_fmaf(-slope2, fabsf(dist), s);
 }
 
+// The lane's row of the kernels over rows: q and dout fragments, δ and lse.
+template <int IO, int DH>
+struct BwdRow {
+  Frag<IO> qf[DH / 16], gf[DH / 16];
+  float delta, lse2;
+  __device__ __forceinline__ void load(const BwdArgs& a, int i, int hq, int h, bool live) {
+    delta = 0.f;
+#pragma unroll
+    for (int s = 0; s < DH / 16; ++s) {
+      const int64_t at = (int64_t)hq * DH + 16 * s + 8 * h;
+      if (i < a.mask.T) {
+        qf[s] = load_frag<IO>(a.q, i * a.ldq + at);
+        gf[s] = load_frag<IO>(a.dout, i * a.lddo + at);
+        float ov[8], gv[8];
+        load8<IO>(a.o, i * a.ldo + at, ov);
+        load8<IO>(a.dout, i * a.lddo + at, gv);
+        if constexpr (IO == kBF16)
+          if (a.rest != nullptr) add_rest(a.rest, (int64_t)i * a.Hq * DH + at, ov);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = __builtin_fmaf(ov[e], gv[e], delta);
+      } else {
+        qf[s] = gf[s] = zero_frag<IO>();
+      }
+    }
+    delta += other_half(delta);
+    lse2 = live ? a.lse[(int64_t)hq * a.mask.T + i] * kLog2e : 0.f;
+    settle(qf);
+    settle(gf);
+    asm volatile("" : "+v"(lse2), "+v"(delta));
+  }
+};
+
+// dq^T += K^T·dS^T of KB blocks of 32 keys from key0 on (`tk`, the values kTile
+// bytes further), masked to the lane's keys [lo, hi) where `partial`.
+template <int IO, int DH, int KB, int MOD, int TILE>
+__device__ __forceinline__ void rows_step(f32x16_t (&acc)[DH / 32], const BwdRow<IO, DH>& row, uint32_t tk, int key0, int lo,
+                                          int hi, bool partial, int i, float slope2, ScoreMod mod) {
+  using T = Tile<IO, DH>;
+  const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h = lane >> 5;
+  const uint32_t ra = T::row_addr(tk, c, h), ca = T::col_addr(tk, lane);
+  const float pre = mod.pre();
+#pragma unroll
+  for (int b = 0; b < KB; ++b) {
+    f32x16_t s, dp;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
+    each<DH / 16>([&](auto n) {
+      s = mma(T::template row_frag<n>(ra, 32 * b * T::kRow), row.qf[n], s);
+      dp = mma(T::template row_frag<n>(ra, TILE + 32 * b * T::kRow), row.gf[n], dp);
+    });
+    const float d0 = (float)(i - key0 - 32 * b - 4 * h);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int k = 8 * (r >> 2) + (r & 3);
+      float sc, dcap = 1.f;
+      if constexpr (MOD != 0)
+        score<IO, MOD>(s[r], pre, mod, slope2, d0 - (float)k, sc, dcap);
+      else
+        sc = s[r] * pre;
+      float ds = exp2_fast(sc - row.lse2) * (dp[r] - row.delta);
+      if constexpr ((MOD & kCapped) != 0) ds *= dcap;
+      s[r] = ds;
+    }
+    if (partial) {
+      int l0 = lo - key0 - 32 * b - 4 * h, h0 = hi - key0 - 32 * b - 4 * h;
+      keep_branch(l0, h0);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int k = 8 * (r >> 2) + (r & 3);
+        s[r] = k >= l0 && k < h0 ? s[r] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const Frag<IO> ds = frag_of<IO>(s, n);
+      each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, (32 * b + 16 * n) * T::kRow), ds, acc[d]); });
+    }
+  }
+}
+
 // Rows: 128 of one query head a workgroup, 32 a wave; key and value tiles of 64.
 template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_kernel(BwdArgs a) {
@@ -79,38 +160,14 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
   if (bhi == 0) blo = 0;
   const bool live = in_doc && lo < hi;
 
-  Frag<IO> qf[DH / 16], gf[DH / 16];
-  float delta = 0.f;
-#pragma unroll
-  for (int s = 0; s < DH / 16; ++s) {
-    const int64_t at = (int64_t)hq * DH + 16 * s + 8 * h;
-    if (i < a.mask.T) {
-      qf[s] = load_frag<IO>(a.q, i * a.ldq + at);
-      gf[s] = load_frag<IO>(a.dout, i * a.lddo + at);
-      float ov[8], gv[8];
-      load8<IO>(a.o, i * a.ldo + at, ov);
-      load8<IO>(a.dout, i * a.lddo + at, gv);
-      if constexpr (IO == kBF16)
-        if (a.rest != nullptr) add_rest(a.rest, (int64_t)i * a.Hq * DH + at, ov);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) delta = __builtin_fmaf(ov[e], gv[e], delta);
-    } else {
-      qf[s] = gf[s] = zero_frag<IO>();
-    }
-  }
-  delta += other_half(delta);
-  float lse2 = 0.f;
-  if (live) lse2 = a.lse[(int64_t)hq * a.mask.T + i] * kLog2e;
-  if (i < a.mask.T && h == 0) a.delta[(int64_t)hq * a.mask.T + i] = live ? delta : 0.f;
+  BwdRow<IO, DH> row;
+  row.load(a, i, hq, h, live);
+  if (i < a.mask.T && h == 0) a.delta[(int64_t)hq * a.mask.T + i] = live ? row.delta : 0.f;
 
   const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
   const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
   Stage<IO, DH, kKeys> sk, sv;
   const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hq] * kLog2e : 0.f;
-  settle(qf);
-  settle(gf);
-  asm volatile("" : "+v"(lse2), "+v"(delta));
-  const float pre = a.mod.pre();
   f32x16_t acc[DH / 32];
 #pragma unroll
   for (int b = 0; b < DH / 32; ++b)
@@ -132,44 +189,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
     __syncthreads();
     if (key0 >= whi || next <= wlo) continue;
     const bool partial = __any(live && (lo > key0 || hi < next));
-    const uint32_t ra = T::row_addr(lds_addr(tk), c, h), ca = T::col_addr(lds_addr(tk), lane);
-#pragma unroll
-    for (int b = 0; b < kKeys / 32; ++b) {
-      f32x16_t s, dp;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
-      each<DH / 16>([&](auto n) {
-        s = mma(T::template row_frag<n>(ra, 32 * b * T::kRow), qf[n], s);
-        dp = mma(T::template row_frag<n>(ra, kTile + 32 * b * T::kRow), gf[n], dp);
-      });
-      const float d0 = (float)(i - key0 - 32 * b - 4 * h);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int k = 8 * (r >> 2) + (r & 3);
-        float sc, dcap = 1.f;
-        if constexpr (MOD != 0)
-          score<IO, MOD>(s[r], pre, a.mod, slope2, d0 - (float)k, sc, dcap);
-        else
-          sc = s[r] * pre;
-        float ds = exp2_fast(sc - lse2) * (dp[r] - delta);
-        if constexpr ((MOD & kCapped) != 0) ds *= dcap;
-        s[r] = ds;
-      }
-      if (partial) {
-        int l0 = lo - key0 - 32 * b - 4 * h, h0 = hi - key0 - 32 * b - 4 * h;
-        keep_branch(l0, h0);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int k = 8 * (r >> 2) + (r & 3);
-          s[r] = k >= l0 && k < h0 ? s[r] : 0.f;
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const Frag<IO> ds = frag_of<IO>(s, n);
-        each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, (32 * b + 16 * n) * T::kRow), ds, acc[d]); });
-      }
-    }
+    rows_step<IO, DH, kKeys / 32, MOD, kTile>(acc, row, lds_addr(tk), key0, lo, hi, partial, i, slope2, a.mod);
   }
   if (i >= a.mask.T || (!in_doc && !a.fill)) return;
 #pragma unroll
@@ -179,6 +199,70 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
       for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
     store_block<IO>(a.dq, i * a.lddq + (int64_t)hq * DH, b, h, acc[b], a.mod.scale);
   }
+}
+
+// The same for grids that would not fill the chip: 32 rows a workgroup, held by
+// all four waves, which take the key tiles of 32 in turn, each through LDS of
+// its own, and add up their sums at the end.
+template <int IO, int DH, int MOD>
+__global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_short_kernel(BwdArgs a) {
+  using T = Tile<IO, DH>;
+  constexpr int kTile = 32 * T::kRow;
+  extern __shared__ __attribute__((aligned(512))) char lds[];
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
+  const int G = a.Hq / a.Hk;
+  const int nt = (a.mask.T + 31) / 32;
+  const int x = blockIdx.x % a.Hq, hk = x % a.Hk, hq = hk * G + x / a.Hk;
+  const int i0 = (nt - 1 - (int)(blockIdx.x / a.Hq)) * 32, i = i0 + c;
+
+  int ba, bb, lo, hi, wlo, whi;
+  a.mask.bounds(i0, i0 + 31, ba, bb);
+  const bool in_doc = a.mask.keys(i, ba, bb, lo, hi);
+  wave_range(lo, hi, wlo, whi);
+  const bool live = in_doc && lo < hi;
+  BwdRow<IO, DH> row;
+  row.load(a, i, hq, h, live);
+  if (i < a.mask.T && wave == 0 && h == 0) a.delta[(int64_t)hq * a.mask.T + i] = live ? row.delta : 0.f;
+
+  const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
+  const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
+  Stage<IO, DH, 32, kWave> sk, sv;
+  const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hq] * kLog2e : 0.f;
+  f32x16_t acc[DH / 32];
+#pragma unroll
+  for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
+  char* tk = lds + wave * 2 * kTile;
+  char* tv = tk + kTile;
+  int key0 = wlo + wave * 32;
+  if (key0 < whi) {
+    sk.load(kb + key0 * a.ldk * T::kElem, a.ldk, whi - key0, lane);
+    sv.load(vb + key0 * a.ldv * T::kElem, a.ldv, whi - key0, lane);
+  }
+  for (; key0 < whi; key0 += 128) {
+    sk.store(tk, lane);
+    sv.store(tv, lane);
+    const int next = key0 + 128;
+    if (next < whi) {
+      sk.load(kb + next * a.ldk * T::kElem, a.ldk, whi - next, lane);
+      sv.load(vb + next * a.ldv * T::kElem, a.ldv, whi - next, lane);
+    }
+    wave_lds_fence();
+    const bool partial = __any(live && (lo > key0 || hi < key0 + 32));
+    rows_step<IO, DH, 1, MOD, kTile>(acc, row, lds_addr(tk), key0, lo, hi, partial, i, slope2, a.mod);
+    wave_lds_fence();
+  }
+  if (!live) {
+#pragma unroll
+    for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
+  }
+  __syncthreads();  // every wave is done with its tiles
+  const f32x16_t sum = sum_waves<DH>(lds, wave, lane, acc, a.mod.scale);
+  if (wave >= DH / 32 || i >= a.mask.T || (!in_doc && !a.fill)) return;
+  store_block<IO>(a.dq, i * a.lddq + (int64_t)hq * DH, wave, h, sum, 1.f);
 }
 
 // Keys: 128 of one key head a workgroup, over the rows that see them, head by
@@ -456,7 +540,9 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
   a.lddq = d.ld_dq;
   a.lddk = d.ld_dk;
   a.lddv = d.ld_dv;
-  const dim3 rows((unsigned)((d.T + kRows - 1) / kRows * d.Hq));
+  const bool small = attn_short(d);
+  const int per = small ? 32 : kRows;
+  const dim3 rows((unsigned)((d.T + per - 1) / per * d.Hq));
   const dim3 keys((unsigned)((d.T + kKeyRows - 1) / kKeyRows * d.Hk * a.pieces));
   hipError_t err = hipErrorInvalidValue;
   dispatch_attn(d.io, d.Dh, d.softcap, d.slopes, [&](auto io_, auto dh_, auto mod_) {
@@ -464,7 +550,11 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
     constexpr int DH = decltype(dh_)::value;
     constexpr int MOD = decltype(mod_)::value;
     constexpr int row = Tile<IO, DH>::kRow;
-    MHC_LAUNCH((attn_bwd_rows_kernel<IO, DH, MOD>), rows, dim3(kThreads), 4 * kKeys * row, s, a);
+    constexpr int few = 8 * 32 * row > wave_states_bytes<DH>() ? 8 * 32 * row : wave_states_bytes<DH>();
+    if (small)
+      MHC_LAUNCH((attn_bwd_rows_short_kernel<IO, DH, MOD>), rows, dim3(kThreads), few, s, a);
+    else
+      MHC_LAUNCH((attn_bwd_rows_kernel<IO, DH, MOD>), rows, dim3(kThreads), 4 * kKeys * row, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return;
     MHC_LAUNCH((attn_bwd_keys_kernel<IO, DH, MOD>), keys, dim3(kKeyThreads), 6 * kQ * row + 8 * 16 * kWave * 4, s, a);

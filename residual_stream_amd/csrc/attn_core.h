@@ -202,15 +202,15 @@ __device__ __forceinline__ void each(F&& f) {
   }
 }
 
-// Staging of R head rows by 256 threads: global memory to registers, then
+// Staging of R head rows by NT threads: global memory to registers, then
 // registers to LDS, so that the next tile is on its way while this one is
-// used.  Thread i takes chunk i mod C of rows i/C, i/C + 256/C, ...
-template <int IO, int DH, int R>
+// used.  Thread i takes chunk i mod C of rows i/C, i/C + NT/C, ...
+template <int IO, int DH, int R, int NT = kThreads>
 struct Stage {
   using T = Tile<IO, DH>;
-  static constexpr int kN = R * T::kChunks / kThreads;  // chunks a thread
-  static constexpr int kStep = kThreads / T::kChunks;   // rows between a thread's chunks
-  static_assert(R * T::kChunks % kThreads == 0 && kThreads % T::kChunks == 0, "whole passes");
+  static constexpr int kN = R * T::kChunks / NT;  // chunks a thread
+  static constexpr int kStep = NT / T::kChunks;   // rows between a thread's chunks
+  static_assert(R * T::kChunks % NT == 0 && NT % T::kChunks == 0, "whole passes");
   u32x4_t w[kN];
 
   // Rows base + 0 .. base + rows - 1, `ld` elements apart; the buffer's own
@@ -348,6 +348,13 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // Ties a branch's compares to the branch: otherwise they are folded into
 // selects that every tile pays for, masked or not.
 __device__ __forceinline__ void keep_branch(int& a, int& b) { asm volatile("" : "+v"(a), "+v"(b)); }
+
+// A wave's own LDS: its writes come before its reads, and these before the
+// next writes, without a barrier.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // How scores are formed from the products q·k, in units of log 2 so that exp2
 // serves: capped (cap·tanh(scale·x/cap), cap > 0), lowered by slope·distance.
@@ -518,6 +525,55 @@ __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH
       const Frag<IO> p = frag_of<IO>(s[b], i);
       each<DH / 32>([&](auto d) { st.o[d] = mma(T::template col_frag<d>(va, (32 * b + 16 * i) * T::kRow), p, st.o[d]); });
     }
+}
+
+// LDS bytes of join_waves / sum_waves.
+template <int DH>
+constexpr int wave_states_bytes() { return 4 * (DH / 32) * 16 * kWave * 4; }
+
+// Sums four waves' accumulators x[block] (scaled by f) for the same 32 columns:
+// wave w < DH/32 returns block w of the sum.  `lds`: wave_states_bytes, free
+// for use by all waves.
+template <int DH>
+__device__ __forceinline__ f32x16_t sum_waves(char* lds, int wave, int lane, const f32x16_t (&x)[DH / 32], float f) {
+  // [wave][column block][element][lane]
+  float* acc = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[((wave * (DH / 32) + b) * 16 + e) * kWave + lane] = x[b][e] * f;
+  __syncthreads();
+  f32x16_t sum;
+  const int b = wave < DH / 32 ? wave : 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) t += acc[((w * (DH / 32) + b) * 16 + e) * kWave + lane];
+    sum[e] = t;
+  }
+  return sum;
+}
+
+// Joins the row states of four waves that held the same 32 rows over different
+// keys: m and l become the whole row's, and wave w < DH/32 returns block w of
+// the unnormalised output.  `stat`: [2][4][32] floats.
+template <int DH>
+__device__ __forceinline__ f32x16_t join_waves(char* lds, float* stat, int wave, int lane, const RowState<DH>& st, float& m,
+                                               float& l) {
+  const int c = lane & 31;
+  const float mine = st.l + other_half(st.l);
+  if (lane < 32) {
+    stat[wave * 32 + c] = st.m;
+    stat[128 + wave * 32 + c] = mine;
+  }
+  __syncthreads();
+  m = fmaxf(fmaxf(stat[c], stat[32 + c]), fmaxf(stat[64 + c], stat[96 + c]));
+  const float base = m == -__builtin_inff() ? 0.f : m;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) l += stat[128 + w * 32 + c] * exp2_fast(stat[w * 32 + c] - base);
+  return sum_waves<DH>(lds, wave, lane, st.o, exp2_fast(st.m - base));
 }
 
 }  // namespace attn

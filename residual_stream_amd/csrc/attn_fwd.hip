@@ -115,7 +115,73 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
     a.lse[(int64_t)hq * a.mask.T + i] = live ? (st.m + __log2f(l)) * kLn2 : -__builtin_inff();
 }
 
+// The same for grids that would not fill the chip: 32 rows a workgroup, held by
+// all four waves, which take the key tiles of 32 in turn, each through LDS of
+// its own (no barrier in the loop), and join their row states at the end.
+template <int IO, int DH, int MOD>
+__global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_short_kernel(FwdArgs a) {
+  using T = Tile<IO, DH>;
+  constexpr int kTile = 32 * T::kRow;
+  extern __shared__ __attribute__((aligned(512))) char lds[];  // a key and a value tile a wave; then the row states
+  __shared__ float stat[256];
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
+  const int G = a.Hq / a.Hk;
+  const int nt = (a.mask.T + 31) / 32;
+  const int x = blockIdx.x % a.Hq, hk = x % a.Hk, hq = hk * G + x / a.Hk;
+  const int i0 = (nt - 1 - (int)(blockIdx.x / a.Hq)) * 32, i = i0 + c;
+
+  int ba, bb, lo, hi, wlo, whi;
+  a.mask.bounds(i0, i0 + 31, ba, bb);
+  const bool in_doc = a.mask.keys(i, ba, bb, lo, hi);
+  wave_range(lo, hi, wlo, whi);
+  const bool live = in_doc && lo < hi;
+
+  Frag<IO> qf[DH / 16];
+#pragma unroll
+  for (int s = 0; s < DH / 16; ++s)
+    qf[s] = i < a.mask.T ? load_frag<IO>(a.q, i * a.ldq + (int64_t)hq * DH + 16 * s + 8 * h) : zero_frag<IO>();
+  const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
+  const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
+  Stage<IO, DH, 32, kWave> sk, sv;
+  const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hq] * kLog2e : 0.f;
+  settle(qf);
+  RowState<DH> st;
+  st.init();
+  char* tk = lds + wave * 2 * kTile;
+  char* tv = tk + kTile;
+  int key0 = wlo + wave * 32;
+  if (key0 < whi) {
+    sk.load(kb + key0 * a.ldk * T::kElem, a.ldk, whi - key0, lane);
+    sv.load(vb + key0 * a.ldv * T::kElem, a.ldv, whi - key0, lane);
+  }
+  for (; key0 < whi; key0 += 128) {
+    sk.store(tk, lane);
+    sv.store(tv, lane);
+    const int next = key0 + 128;
+    if (next < whi) {
+      sk.load(kb + next * a.ldk * T::kElem, a.ldk, whi - next, lane);
+      sv.load(vb + next * a.ldv * T::kElem, a.ldv, whi - next, lane);
+    }
+    wave_lds_fence();
+    const bool partial = __any(live && (lo > key0 || hi < key0 + 32));
+    attend<IO, DH, 1, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, lo, hi, partial, i, slope2, a.mod);
+    wave_lds_fence();
+  }
+  if (!live) st.init();
+  float m, l;
+  const f32x16_t sum = join_waves<DH>(lds, stat, wave, lane, st, m, l);
+  if (wave >= DH / 32 || i >= a.mask.T || (!in_doc && !a.fill)) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  store_block<IO>(a.o, i * a.ldo + (int64_t)hq * DH, wave, h, sum, inv);
+  if constexpr (IO == kBF16)
+    if (a.rest != nullptr) store_rest(a.rest, ((int64_t)i * a.Hq + hq) * DH, wave, h, sum, inv);
+  if (a.lse != nullptr && wave == 0 && h == 0)
+    a.lse[(int64_t)hq * a.mask.T + i] = live ? (m + __log2f(l)) * kLn2 : -__builtin_inff();
+}
+
 }  // namespace
+
+bool attn_short(const mhc_attn_desc& d) { return (d.T + kRows - 1) / kRows * d.Hq < device_cu_count(); }
 
 attn::DocMask doc_mask(const mhc_attn_desc& d) {
   attn::DocMask m;
@@ -147,14 +213,20 @@ hipError_t launch_attn(const mhc_attn_desc& d, const void* q, const void* k, con
   a.ldk = d.ldk;
   a.ldv = d.ldv;
   a.ldo = d.ldo;
-  const dim3 grid((unsigned)((d.T + kRows - 1) / kRows * d.Hq));
+  const bool small = attn_short(d);
+  const int rows = small ? 32 : kRows;
+  const dim3 grid((unsigned)((d.T + rows - 1) / rows * d.Hq));
   hipError_t err = hipErrorInvalidValue;
   dispatch_attn(d.io, d.Dh, d.softcap, d.slopes, [&](auto io_, auto dh_, auto mod_) {
     constexpr int IO = decltype(io_)::value;
     constexpr int DH = decltype(dh_)::value;
     constexpr int MOD = decltype(mod_)::value;
-    constexpr int lds = 4 * kKeys * Tile<IO, DH>::kRow;
-    MHC_LAUNCH((attn_fwd_kernel<IO, DH, MOD>), grid, dim3(kThreads), lds, s, a);
+    constexpr int row = Tile<IO, DH>::kRow;
+    constexpr int few = 8 * 32 * row > wave_states_bytes<DH>() ? 8 * 32 * row : wave_states_bytes<DH>();
+    if (small)
+      MHC_LAUNCH((attn_fwd_short_kernel<IO, DH, MOD>), grid, dim3(kThreads), few, s, a);
+    else
+      MHC_LAUNCH((attn_fwd_kernel<IO, DH, MOD>), grid, dim3(kThreads), 4 * kKeys * row, s, a);
     err = hipGetLastError();
   });
   return err;

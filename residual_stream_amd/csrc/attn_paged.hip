@@ -206,7 +206,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
   using T = Tile<IO, DH>;
   constexpr int kTile = kFewKeys * T::kRow;
   extern __shared__ __attribute__((aligned(512))) char lds[];  // a key and a value tile a wave; then the waves' row states
-  __shared__ float wm[4][32], wl[4][32];
+  __shared__ float stat[256];
   __shared__ int any_bad;
   fill_rest<IO, DH>(a);
   const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
@@ -243,45 +243,16 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
     sg.store(tk, tv, lane);
     if (key0 + kAll < hi) sg.load(a, hk, lane, key0 + kAll, hi - 1, bad);
     if (key0 + 2 * kAll < hi) sg.lookup(a, table, lane, key0 + 2 * kAll, hi - 1);
-    // the wave's own LDS: its writes come before its reads
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_fence();
     const bool partial = __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kFewKeys)) || key0 + kFewKeys > hi;
     attend<IO, DH, 1, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, r.lo, min(r.hi, hi), partial, r.pos, slope2, a.mod);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_fence();
   }
   if (__any(bad) && lane == 0) any_bad = 1;
   if (r.lo >= r.hi) st.init();  // (unmasked tiles were not for this row)
-  // join the four waves' states
-  float l = st.l + other_half(st.l);
-  if (h == 0) {
-    wm[wave][c] = st.m;
-    wl[wave][c] = l;
-  }
-  __syncthreads();
-  float m = fmaxf(fmaxf(wm[0][c], wm[1][c]), fmaxf(wm[2][c], wm[3][c]));
-  const float base = m == -__builtin_inff() ? 0.f : m;
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) l += wl[w][c] * exp2_fast(wm[w][c] - base);
-  const float f = exp2_fast(st.m - base);
-  // [wave][column block][element][lane]: each wave adds up one column block
-  float* acc = reinterpret_cast<float*>(lds);
-#pragma unroll
-  for (int b = 0; b < DH / 32; ++b)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[((wave * (DH / 32) + b) * 16 + e) * kWave + lane] = st.o[b][e] * f;
-  __syncthreads();
+  float m, l;
+  const f32x16_t sum = join_waves<DH>(lds, stat, wave, lane, st, m, l);
   if (wave >= DH / 32 || !r.real) return;
-  f32x16_t sum;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) t += acc[((w * (DH / 32) + wave) * 16 + e) * kWave + lane];
-    sum[e] = t;
-  }
   float inv = l == 0.f ? 0.f : 1.f / l;
   if (any_bad) inv = __builtin_nanf("");
   if (a.splits == 1) {
@@ -359,41 +330,56 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
   finish<IO, DH>(a, r, sp, h, st, st.l + other_half(st.l), any_bad != 0);
 }
 
-// Joins the splits' partial rows: one wave a row of [sequence][c][head].
+// Joins the splits' partial rows: Dh/4 lanes a row of [sequence][c][head], four
+// elements each, with a running maximum over the splits, eight of them in
+// flight at a time.
 template <int IO, int DH>
 __global__ __launch_bounds__(kThreads) void attn_paged_join_kernel(PagedArgs a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t n = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
+  constexpr int kLanes = DH / 4;
+  const int64_t n = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const int e = threadIdx.x % kLanes * 4;
   const int64_t sc = n / a.Hq;
   const int s = (int)(sc / a.max_q), c = (int)(sc % a.max_q), hq = (int)(n % a.Hq);
   if (s >= a.n) return;
   const Seq q = seq_of(a, s);
   if (c >= q.nq) return;
   const int64_t row = (q.t0 + c) * a.Hq + hq, all = a.T * a.Hq;
-  const float mine = lane < a.splits ? a.part_l[lane * all + row] : -__builtin_inff();
-  float m = mine;
+  float m = -__builtin_inff(), total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int kAhead = 8;
+  for (int i = 0; i < a.splits; i += kAhead) {
+    float l[kAhead];
+    float4 v[kAhead];
 #pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
-  const float w = exp2_fast(mine - (m == -__builtin_inff() ? 0.f : m));
-  const float total = wave_sum(w);
-  constexpr int kPer = DH / kWave;
-  float acc[kPer];
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t at = min(i + j, a.splits - 1) * all + row;
+      l[j] = i + j < a.splits ? a.part_l[at] : -__builtin_inff();
+      v[j] = *reinterpret_cast<const float4*>(a.part_o + at * DH + e);
+    }
+    float top = m;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int i = 0; i < a.splits; ++i) {
-    const float wi = __shfl(w, i, kWave);
+    for (int j = 0; j < kAhead; ++j) top = fmaxf(top, l[j]);
+    const float base = top == -__builtin_inff() ? 0.f : top, f = exp2_fast(m - base);
+    m = top;
+    total *= f;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = __builtin_fmaf(wi, a.part_o[(i * all + row) * DH + lane + e * kWave], acc[e]);
+    for (int k = 0; k < 4; ++k) acc[k] *= f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const float w = exp2_fast(l[j] - base);
+      total += w;
+      acc[0] = __builtin_fmaf(w, v[j].x, acc[0]);
+      acc[1] = __builtin_fmaf(w, v[j].y, acc[1]);
+      acc[2] = __builtin_fmaf(w, v[j].z, acc[2]);
+      acc[3] = __builtin_fmaf(w, v[j].w, acc[3]);
+    }
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int64_t at = (q.t0 + c) * a.ldo + (int64_t)hq * DH + lane + e * kWave;
-    if constexpr (IO == kBF16)
-      static_cast<uint16_t*>(a.o)[at] = (uint16_t)f32_to_bf16_bits(acc[e] * inv);
-    else
-      static_cast<float*>(a.o)[at] = acc[e] * inv;
-  }
+  const int64_t at = (q.t0 + c) * a.ldo + (int64_t)hq * DH + e;
+  if constexpr (IO == kBF16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + at) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
 }
 
 bool few_rows(const mhc_paged_desc& d) { return (int64_t)d.max_q * (d.Hq / d.Hk) <= kFewRows; }
@@ -401,13 +387,17 @@ int row_tiles(const mhc_paged_desc& d) {
   return few_rows(d) ? 1 : (int)(((int64_t)d.max_q * (d.Hq / d.Hk) + kRows - 1) / kRows);
 }
 
-// Splits of the keys: enough workgroups for every CU to hold two, none with
-// fewer than 128 keys (few rows) or 512 (many) of a full table.
+// Splits of the keys: workgroups for every CU twice over with few rows, and a
+// half more than fit with many (64 sequences of up to 8192 keys, single tokens:
+// 273 + 6 us for the join with four workgroups a CU, 285 with two and no join;
+// 700 tokens over 6000 keys: 104 + 11 us with three a CU, 131 + 10 with two,
+// 121 + 12 with four), none with fewer than 128 keys (few) or 256 (many) of a
+// full table.
 int splits_of(const mhc_paged_desc& d) {
   const int64_t base = (int64_t)d.n_seqs * d.Hk * row_tiles(d);
   const int64_t keys = (int64_t)d.max_pages * d.page_size;
-  int64_t want = (2 * device_cu_count() + base - 1) / base;
-  const int64_t most = (keys + (few_rows(d) ? 127 : 511)) / (few_rows(d) ? 128 : 512);
+  int64_t want = ((few_rows(d) ? 4 : 3) * device_cu_count() + base - 1) / base;
+  const int64_t most = (keys + (few_rows(d) ? 127 : 255)) / (few_rows(d) ? 128 : 256);
   if (want > most) want = most;
   if (want > kMaxSplits) want = kMaxSplits;
   return want < 1 ? 1 : (int)want;
@@ -462,7 +452,7 @@ hipError_t launch_attn_paged(const mhc_paged_desc& d, const void* q, const void*
     constexpr int MOD = decltype(mod_)::value;
     constexpr int row = Tile<IO, DH>::kRow;
     // few: four waves' tiles, or their fp32 row states
-    constexpr int few_lds = 4 * 2 * kFewKeys * row > 4 * 32 * DH * 4 ? 4 * 2 * kFewKeys * row : 4 * 32 * DH * 4;
+    constexpr int few_lds = 8 * kFewKeys * row > wave_states_bytes<DH>() ? 8 * kFewKeys * row : wave_states_bytes<DH>();
     if (few)
       MHC_LAUNCH((attn_paged_few_kernel<IO, DH, MOD>), grid, dim3(kThreads), few_lds, s, a);
     else
@@ -470,7 +460,7 @@ hipError_t launch_attn_paged(const mhc_paged_desc& d, const void* q, const void*
     err = hipGetLastError();
     if (err != hipSuccess || a.splits == 1) return;
     const int64_t rows = (int64_t)d.n_seqs * d.max_q * d.Hq;
-    MHC_LAUNCH((attn_paged_join_kernel<IO, DH>), dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, s, a);
+    MHC_LAUNCH((attn_paged_join_kernel<IO, DH>), dim3((unsigned)((rows * (DH / 4) + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a);
     err = hipGetLastError();
   });
   return err;
