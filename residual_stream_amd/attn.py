@@ -252,7 +252,7 @@ def _saved(saved, d, dev):
 
 
 def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=0.0, slopes=None, scale=None, out=None,
-             stream=None):
+             fill_outside=None, stream=None):
     """Attention of q[T,Hq,Dh] over k, v[T,Hk,Dh] (Dh 64 or 128) of a packed
     batch: docs (int32 [n+1], sorted) holds the documents' first rows and the
     end of the last, None is one document of all rows.  Row i sees its own
@@ -264,11 +264,12 @@ def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=
     Returns (o[T,Hq,Dh], saved), ``saved`` an fp32 tensor of
     :func:`saved_floats` elements for the backward; its first Hq·T are the rows'
     log-sum-exps [Hq, T].  Rows of no document come out as zeros (lse -inf); in
-    tensors passed as ``out=(o, saved or None)`` they are left as they were."""
+    tensors passed as ``out=(o, saved or None)`` they are left as they were,
+    unless fill_outside is true."""
     lib = load()
     d, _ks, at, dtype, dev = _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
+    d.fill_outside = 1 if (out is None if fill_outside is None else fill_outside) else 0
     if out is None:
-        d.fill_outside = 1
         out = (torch.empty(q.shape, dtype=dtype, device=q.device),
                torch.empty(saved_floats(d.T, d.Hq, d.Dh, d.io), dtype=torch.float32, device=q.device))
     o, saved = out
@@ -279,18 +280,18 @@ def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=
 
 
 def mhc_attn_bwd(do, q, k, v, o, saved, *, docs=None, causal=True, prefix=None, window=0, softcap=0.0, slopes=None,
-                 scale=None, out=None, workspace=None, stream=None):
+                 scale=None, out=None, fill_outside=None, workspace=None, stream=None):
     """Backward of :func:`mhc_attn` from its inputs and results: returns (dq, dk,
     dv), dk and dv summed over the query heads that share a key head.  Rows of
-    no document get zeros, or are left as they were in tensors passed as
-    ``out``."""
+    no document get zeros; in tensors passed as ``out`` they are left as they
+    were, unless fill_outside is true."""
     lib = load()
     d, ks, at, dtype, dev = _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
     d.ld_do = _heads("do", do, q.shape, dtype, dev)
     d.ldo = _heads("o", o, q.shape, dtype, dev)
     lse, rest = _saved(saved, d, dev)
+    d.fill_outside = 1 if (out is None if fill_outside is None else fill_outside) else 0
     if out is None:
-        d.fill_outside = 1
         out = tuple(torch.empty(s, dtype=dtype, device=q.device) for s in (q.shape, ks, ks))
     dq, dk, dv = out
     d.ld_dq = _heads("dq", dq, q.shape, dtype, dev)

@@ -39,16 +39,24 @@ computed once per step; the per-token work stays in the kernels.
 read run as one fused call (`mhc_post_pre`, the pages' inference fusion),
 with the same results as the blocks run one after another.
 
+`MHCAttention` is a sublayer for these blocks: projections around the
+library's query/key norm with rotation and its masked attention
+(:mod:`residual_stream_amd.attn`), for training on packed documents and for
+serving over a paged cache.
+
 Every per-token step runs in the library's kernels; this module only wires
 them into autograd.  It needs a GPU and the built library, like the binding.
 """
 
 from __future__ import annotations
 
+import itertools
+
 import torch
+from torch.autograd.function import once_differentiable
 from torch.utils.checkpoint import checkpoint
 
-from . import mhc
+from . import attn, mhc
 
 
 class _DxHandoff:
@@ -299,3 +307,151 @@ class MHCStack(torch.nn.Module):
             else:
                 x = _Post.apply(x, y, Hq, Hr, None, None, b.eps, handoff)
         return x.reshape(shape)
+
+
+class AttnBatch:
+    """The tokens that the `MHCAttention` layers of a model see in a training or
+    prefill pass: positions[T] (int32), docs (int32 [n+1], sorted, the first rows
+    of the packed documents and the end of the last; None: one document) and
+    prefix (int32 [n] or None).  Made once for a batch, shared by the layers."""
+
+    def __init__(self, positions, docs=None, prefix=None):
+        self.positions, self.docs, self.prefix = positions, docs, prefix
+
+    @classmethod
+    def packed(cls, lengths, prefix=None, device="cuda"):
+        """Documents of the given lengths one after another, each counted from 0."""
+        ints = lambda a: torch.tensor(list(a), dtype=torch.int32, device=device)  # noqa: E731
+        pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in lengths]).to(device)
+        return cls(pos, ints(itertools.accumulate(lengths, initial=0)), None if prefix is None else ints(prefix))
+
+
+class CacheBatch:
+    """New tokens of sequences whose earlier ones lie in the layers' paged caches
+    (`MHCAttention.new_cache`): positions[T] and slots[T] (int64) of the tokens,
+    packed by sequence, the page tables pages[n, max_pages], kv_lens[n] with the
+    new tokens, cu_q[n+1] with max_q for chunks (None: one token each), and
+    prefix[n] or None."""
+
+    def __init__(self, positions, slots, pages, kv_lens, cu_q=None, max_q=None, prefix=None):
+        self.positions, self.slots, self.pages, self.kv_lens = positions, slots, pages, kv_lens
+        self.cu_q, self.max_q, self.prefix = cu_q, max_q, prefix
+
+    @classmethod
+    def step(cls, pages, done, new, page_size, prefix=None):
+        """The next new[s] tokens (host numbers) of sequences that have done[s] in the cache."""
+        dev = pages.device
+        if any(n > 0 and -(-(d + n) // page_size) > pages.shape[1] for d, n in zip(done, new)):
+            raise ValueError("a sequence outgrows its page table")
+        seq = torch.tensor([s for s, n in enumerate(new) for _ in range(n)], device=dev)
+        pos = torch.tensor([p for d, n in zip(done, new) for p in range(d, d + n)], device=dev)
+        slots = pages[seq, pos // page_size].long() * page_size + pos % page_size
+        ints = lambda a: torch.tensor(list(a), dtype=torch.int32, device=dev)  # noqa: E731
+        one = all(n == 1 for n in new)
+        return cls(pos.int(), slots, pages, ints(d + n for d, n in zip(done, new)),
+                   None if one else ints(itertools.accumulate(new, initial=0)), None if one else max(max(new), 1),
+                   None if prefix is None else ints(prefix))
+
+
+class _Attention(torch.autograd.Function):
+    """q, k and v side by side in qkv[T, (Hq+2Hk)·Dh] to o[T, Hq·Dh]: norm and
+    rotation of q and k, then attention.  The backward keeps qkv, the rotated q
+    and k, o and the attention's saved tensor, and writes the three gradients
+    into one tensor of qkv's shape."""
+
+    @staticmethod
+    def forward(ctx, qkv, q_weight, k_weight, freqs, slopes, positions, docs, prefix, heads, rope, scores):
+        q, k, v = _split(qkv, heads)
+        qr, kr = attn.mhc_qk_rope(q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight, **rope)
+        o, saved = attn.mhc_attn(qr, kr, v, docs=docs, prefix=prefix, slopes=slopes, **scores)
+        ctx.save_for_backward(qkv, q_weight, k_weight, freqs, slopes, positions, docs, prefix, qr, kr, o, saved)
+        ctx.cfg = (heads, rope, scores)
+        return o.flatten(1)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do):
+        qkv, q_weight, k_weight, freqs, slopes, positions, docs, prefix, qr, kr, o, saved = ctx.saved_tensors
+        heads, rope, scores = ctx.cfg
+        q, k, v = _split(qkv, heads)
+        dqkv = torch.empty_like(qkv)
+        dq, dk, dv = _split(dqkv, heads)
+        dqr, dkr = torch.empty_like(qr), torch.empty_like(kr)
+        attn.mhc_attn_bwd(do.contiguous().view(o.shape), qr, kr, v, o, saved, docs=docs, prefix=prefix, slopes=slopes,
+                          out=(dqr, dkr, dv), fill_outside=True, **scores)
+        dqw, dkw = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        attn.mhc_qk_rope_bwd(dqr, dkr, q, k, positions, freqs, q_weight=q_weight, k_weight=k_weight,
+                             out=(dq, dk, dqw, dkw), **rope)
+        return dqkv, dqw, dkw, None, None, None, None, None, None, None, None
+
+
+def _split(qkv, heads):
+    """q[T,Hq,Dh], k[T,Hk,Dh] and v[T,Hk,Dh] of qkv[T, (Hq+2Hk)·Dh], as views."""
+    Hq, Hk, Dh = heads
+    return (qkv[:, :Hq * Dh].unflatten(1, (Hq, Dh)), qkv[:, Hq * Dh:(Hq + Hk) * Dh].unflatten(1, (Hk, Dh)),
+            qkv[:, (Hq + Hk) * Dh:].unflatten(1, (Hk, Dh)))
+
+
+class MHCAttention(torch.nn.Module):
+    """An attention sublayer h[T, hidden] → y[T, hidden] for `MHCBlock`: one
+    projection to q, k and v, the per-head norm of q and k with the rotation of
+    their first `rotated` elements, masked attention, and the output projection.
+
+    ``batch`` says what the T tokens are and is set before the pass: an
+    `AttnBatch` for training (gradients through every step), or a `CacheBatch`
+    for serving, where the new keys and values go to the layer's own cache
+    (`new_cache`) and attention reads it.  window, softcap, slopes (fp32
+    [heads], a constant) and causal=False are as in `attn.mhc_attn`; a
+    CacheBatch is causal.
+
+    Parameters: qkv[(heads + 2·key_heads)·head_dim, hidden] and out[hidden,
+    heads·head_dim] in `dtype`, q_weight and k_weight [head_dim] in fp32.
+    """
+
+    def __init__(self, hidden: int, heads: int, key_heads: int, head_dim: int, *, rotated: int | None = None,
+                 base: float = 10000.0, interleaved: bool = False, eps: float = 1e-6, causal: bool = True, window: int = 0,
+                 softcap: float = 0.0, slopes=None, scale: float | None = None, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        if heads % key_heads:
+            raise ValueError(f"{heads} query heads cannot share {key_heads} key heads evenly")
+        self.heads = (heads, key_heads, head_dim)
+        width = (heads + 2 * key_heads) * head_dim
+        self.qkv = torch.nn.Parameter((torch.randn(width, hidden, device=device) / hidden ** 0.5).to(dtype))
+        self.out = torch.nn.Parameter((torch.randn(hidden, heads * head_dim, device=device) / (heads * head_dim) ** 0.5).to(dtype))
+        self.q_weight = torch.nn.Parameter(torch.ones(head_dim, device=device))
+        self.k_weight = torch.nn.Parameter(torch.ones(head_dim, device=device))
+        self.register_buffer("freqs", attn.rope_freqs(rotated or head_dim, base, device), persistent=False)
+        self.register_buffer("slopes", slopes, persistent=False)
+        self.rope = dict(eps=eps, interleaved=interleaved)
+        self.scores = dict(window=window, softcap=softcap, scale=scale)
+        self.causal = causal
+        self.batch = None
+        self.k_cache = self.v_cache = None
+
+    def new_cache(self, num_pages: int, page_size: int):
+        """Gives the layer an empty cache of num_pages pages of page_size tokens."""
+        _, Hk, Dh = self.heads
+        make = lambda: torch.zeros((num_pages, page_size, Hk, Dh), dtype=self.qkv.dtype, device=self.qkv.device)  # noqa: E731
+        self.k_cache, self.v_cache = make(), make()
+
+    def forward(self, h):
+        b = self.batch
+        if b is None:
+            raise RuntimeError("set `batch` (AttnBatch or CacheBatch) before the pass")
+        qkv = torch.nn.functional.linear(h, self.qkv)
+        if isinstance(b, CacheBatch):
+            if torch.is_grad_enabled() and qkv.requires_grad:
+                raise RuntimeError("a CacheBatch takes no gradients: run it under torch.no_grad()")
+            if self.k_cache is None:
+                raise RuntimeError("the layer has no cache: call new_cache first")
+            if not self.causal:
+                raise RuntimeError("a CacheBatch is causal")
+            q, k, v = _split(qkv, self.heads)
+            q = attn.mhc_qk_rope_cache(q, k, v, b.positions, self.freqs, self.k_cache, self.v_cache, b.slots,
+                                       q_weight=self.q_weight, k_weight=self.k_weight, **self.rope)
+            o = attn.mhc_attn_paged(q, self.k_cache, self.v_cache, b.pages, b.kv_lens, cu_q=b.cu_q, max_q=b.max_q,
+                                    prefix=b.prefix, slopes=self.slopes, **self.scores).flatten(1)
+        else:
+            o = _Attention.apply(qkv, self.q_weight, self.k_weight, self.freqs, self.slopes, b.positions, b.docs, b.prefix,
+                                 self.heads, self.rope, dict(self.scores, causal=self.causal))
+        return torch.nn.functional.linear(o, self.out)
