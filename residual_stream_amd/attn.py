@@ -103,6 +103,11 @@ def _key_shape(k, q_shape):
     return torch.Size((q_shape[0], Hk, q_shape[2]))
 
 
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _stream_of(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -113,6 +118,7 @@ def _scratch(need, workspace, device):
         if not need:
             return None, 0, None
         workspace = _workspace(need, device)
+        return workspace.data_ptr(), need, workspace
     return workspace.data_ptr(), _ws_bytes(workspace), workspace
 
 
@@ -148,10 +154,12 @@ def mhc_qk_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-
     lib = load()
     d, ks, at, dtype, dev = _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
     if out is None:
-        out = (torch.empty(q.shape, dtype=dtype, device=q.device), torch.empty(ks, dtype=dtype, device=q.device))
-    qo, ko = out
-    d.ldq_out = _heads("q_out", qo, q.shape, dtype, dev)
-    d.ldk_out = _heads("k_out", ko, ks, dtype, dev)
+        out = (_like(q), _like(k))
+        qo, ko = out
+    else:
+        qo, ko = out
+        d.ldq_out = _heads("q_out", qo, q.shape, dtype, dev)
+        d.ldk_out = _heads("k_out", ko, ks, dtype, dev)
     _check(lib.mhc_qk_rope(_ref(d), *at, qo.data_ptr(), ko.data_ptr(), _stream_of(stream, dev)), "mhc_qk_rope")
     return out
 
@@ -166,17 +174,17 @@ def mhc_qk_rope_bwd(dq_out, dk_out, q, k, positions, freqs, *, q_weight=None, k_
     d.ldq_out = _heads("dq_out", dq_out, q.shape, dtype, dev)
     d.ldk_out = _heads("dk_out", dk_out, ks, dtype, dev)
     if out is None:
-        out = (torch.empty(q.shape, dtype=dtype, device=q.device), torch.empty(ks, dtype=dtype, device=q.device),
-               None if q_weight is None else torch.empty_like(q_weight),
-               None if k_weight is None else torch.empty_like(k_weight))
-    dq, dk, dqw, dkw = out
-    d.ld_dq = _heads("dq", dq, q.shape, dtype, dev)
-    d.ld_dk = _heads("dk", dk, ks, dtype, dev)
-    for name, g, w in (("dq_weight", dqw, q_weight), ("dk_weight", dkw, k_weight)):
-        if g is not None and w is None:
-            raise ValueError(f"{name} without the weight itself")
-    row = (q.shape[2],)
-    grads = (_vec("dq_weight", dqw, row, torch.float32, dev), _vec("dk_weight", dkw, row, torch.float32, dev))
+        out = (_like(q), _like(k), None if q_weight is None else _like(q_weight), None if k_weight is None else _like(k_weight))
+        dq, dk, dqw, dkw = out
+        grads = (None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr())
+    else:
+        dq, dk, dqw, dkw = out
+        d.ld_dq = _heads("dq", dq, q.shape, dtype, dev)
+        d.ld_dk = _heads("dk", dk, ks, dtype, dev)
+        if (dqw is not None and q_weight is None) or (dkw is not None and k_weight is None):
+            raise ValueError("a weight's gradient without the weight itself")
+        row = (q.shape[2],)
+        grads = (_vec("dq_weight", dqw, row, torch.float32, dev), _vec("dk_weight", dkw, row, torch.float32, dev))
     ws, nbytes, _keep = _scratch(lib.mhc_qk_rope_bwd_workspace_bytes(_ref(d)), workspace, q.device)
     _check(lib.mhc_qk_rope_bwd(_ref(d), dq_out.data_ptr(), dk_out.data_ptr(), *at, dq.data_ptr(), dk.data_ptr(), *grads,
                                ws, nbytes, _stream_of(stream, dev)), "mhc_qk_rope_bwd")
@@ -205,8 +213,9 @@ def mhc_qk_rope_cache(q, k, v, positions, freqs, k_cache, v_cache, slots, *, q_w
     pages, size, kc, vc = _cache(k_cache, v_cache, ks[1], ks[2], dtype, dev)
     to = _vec("slots", _need("slots", slots), (ks[0],), torch.int64, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=q.device)
-    d.ldq_out = _heads("q_out", out, q.shape, dtype, dev)
+        out = _like(q)
+    else:
+        d.ldq_out = _heads("q_out", out, q.shape, dtype, dev)
     _check(lib.mhc_qk_rope_cache(_ref(d), at[0], at[1], v.data_ptr(), *at[2:], out.data_ptr(), kc, vc, to, pages * size,
                                  _stream_of(stream, dev)), "mhc_qk_rope_cache")
     return out
@@ -270,10 +279,11 @@ def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=
     d, _ks, at, dtype, dev = _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
     d.fill_outside = 1 if (out is None if fill_outside is None else fill_outside) else 0
     if out is None:
-        out = (torch.empty(q.shape, dtype=dtype, device=q.device),
-               torch.empty(saved_floats(d.T, d.Hq, d.Dh, d.io), dtype=torch.float32, device=q.device))
-    o, saved = out
-    d.ldo = _heads("o", o, q.shape, dtype, dev)
+        out = (_like(q), q.new_empty(saved_floats(d.T, d.Hq, d.Dh, d.io), dtype=torch.float32))
+        o, saved = out
+    else:
+        o, saved = out
+        d.ldo = _heads("o", o, q.shape, dtype, dev)
     lse, rest = (None, None) if saved is None else _saved(saved, d, dev)
     _check(lib.mhc_attn(_ref(d), *at, o.data_ptr(), lse, rest, _stream_of(stream, dev)), "mhc_attn")
     return out
@@ -292,11 +302,13 @@ def mhc_attn_bwd(do, q, k, v, o, saved, *, docs=None, causal=True, prefix=None, 
     lse, rest = _saved(saved, d, dev)
     d.fill_outside = 1 if (out is None if fill_outside is None else fill_outside) else 0
     if out is None:
-        out = tuple(torch.empty(s, dtype=dtype, device=q.device) for s in (q.shape, ks, ks))
-    dq, dk, dv = out
-    d.ld_dq = _heads("dq", dq, q.shape, dtype, dev)
-    d.ld_dk = _heads("dk", dk, ks, dtype, dev)
-    d.ld_dv = _heads("dv", dv, ks, dtype, dev)
+        out = (_like(q), _like(k), _like(v))
+        dq, dk, dv = out
+    else:
+        dq, dk, dv = out
+        d.ld_dq = _heads("dq", dq, q.shape, dtype, dev)
+        d.ld_dk = _heads("dk", dk, ks, dtype, dev)
+        d.ld_dv = _heads("dv", dv, ks, dtype, dev)
     ws, nbytes, _keep = _scratch(lib.mhc_attn_bwd_workspace_bytes(_ref(d)), workspace, q.device)
     _check(lib.mhc_attn_bwd(_ref(d), do.data_ptr(), *at, o.data_ptr(), lse, rest, dq.data_ptr(), dk.data_ptr(),
                             dv.data_ptr(), ws, nbytes, _stream_of(stream, dev)), "mhc_attn_bwd")
@@ -344,8 +356,9 @@ def mhc_attn_paged(q, k_cache, v_cache, pages, kv_lens, *, cu_q=None, max_q=None
                      _vec("pages", pages, (n, width), torch.int32, dev), _vec("prefix", prefix, (n,), torch.int32, dev),
                      _slopes(slopes, Hq, dev), _heads("q", q, shape, dtype, dev), Hq * Dh)
     if out is None:
-        out = (torch.empty if n else torch.zeros)(shape, dtype=dtype, device=q.device)
-    d.ldo = _heads("o", out, shape, dtype, dev)
+        out = _like(q) if n else torch.zeros_like(q, memory_format=torch.contiguous_format)
+    else:
+        d.ldo = _heads("o", out, shape, dtype, dev)
     ws, nbytes, _keep = _scratch(lib.mhc_attn_paged_workspace_bytes(_ref(d)), workspace, q.device)
     _check(lib.mhc_attn_paged(_ref(d), q.data_ptr(), kc, vc, out.data_ptr(), ws, nbytes, _stream_of(stream, dev)),
            "mhc_attn_paged")

@@ -23,7 +23,7 @@ bool attn_short(const mhc_attn_desc& d);
 namespace {
 
 constexpr int kRows = 128, kKeys = 64;   // dq: rows of a workgroup, keys of a tile
-constexpr int kKeyRows = 128, kQ = 32;   // dk, dv: keys of a workgroup, rows of a tile
+constexpr int kKeyRows = 128;            // dk, dv: keys of a workgroup
 constexpr int kMaxPieces = 16;
 
 struct BwdArgs {
@@ -266,19 +266,17 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_s
 }
 
 // Keys: 128 of one key head a workgroup, over the rows that see them, head by
-// head of the group, in tiles of 32.  Scores here are S = Q·K^T with the keys
-// as columns, so that P and dS are the B operands of dv^T = dO^T·P and
+// head of the group, in tiles of Q rows.  Scores here are S = Q·K^T with the
+// keys as columns, so that P and dS are the B operands of dv^T = dO^T·P and
 // dk^T = Q^T·dS.
 //
 // Eight waves: a pair for every 32 keys, on the same SIMD.  The first wave of
 // a pair forms S and P and sums dv; the second forms dP, takes P from LDS one
-// tile later, and sums dk.  Each then holds one accumulator and one set of key
-// fragments, which leaves room for two waves a SIMD, one of which can use the
-// matrix cores while the other is at its exponentials (one wave a SIMD with
-// both sums: 2.4 ms at T = 8192, 40/8 heads of 128, bf16; two waves a SIMD
-// with both sums: spills, 4.2 ms).  One barrier a tile: tile n is in
-// use by the first waves while the second are at n - 1, so tiles have three
-// buffers and P two.
+// tile later and sums dk.  Each then holds one accumulator and one set of key
+// fragments, which leaves room for two waves a SIMD, and the second does its
+// vector work (dS of tile n - 1) while the first is at its products (S of tile
+// n), and the other way round.  One barrier a tile: tile n is in use by the
+// first waves while the second are at q of n - 1 and dout of n.
 //
 // The (head, row tile) steps of a key tile are cut into `pieces` for
 // workgroups of their own where the key tiles are too few to fill the chip;
@@ -286,17 +284,13 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_s
 // order.
 constexpr int kKeyThreads = 512;
 
-template <int IO, int DH, int MOD>
-__global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a) {
+template <int IO, int DH, int MOD, int Q, bool SECOND>
+__device__ __forceinline__ void keys_wave(const BwdArgs& a, char* lds, int* range,
+                                          float (*stat)[2][Q], int pair, int lane, int thread) {
   using T = Tile<IO, DH>;
-  constexpr int kTile = kQ * T::kRow;
-  // three buffers of a row tile's q and dout, then P of two tiles for each pair
-  extern __shared__ __attribute__((aligned(512))) char lds[];
-  __shared__ int range[8];
-  __shared__ float stat[3][2][kQ];  // [buffer][lse in log 2 units, δ][row]
-  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
-  const int pair = wave & 3;
-  const bool second = wave >= 4;  // (the same for the whole wave)
+  constexpr int QB = Q / 32;
+  constexpr int kTile = Q * T::kRow;
+  const int c = lane & 31, h = lane >> 5;
   const int G = a.Hq / a.Hk;
   const int hk = blockIdx.x % a.Hk, piece = blockIdx.x / a.Hk % a.pieces, tile = blockIdx.x / a.Hk / a.pieces;
   const int j0 = tile * kKeyRows + pair * 32, j = j0 + c;
@@ -305,22 +299,22 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
   a.mask.bounds(j0, j0 + 31, ba, bb);
   const bool in_doc = a.mask.rows(j, ba, bb, lo, hi);
   wave_range(lo, hi, wlo, whi);
-  if (!second && lane == 0) {
+  if (!SECOND && lane == 0) {
     range[pair] = whi > 0 ? wlo : 0x7fffffff;
     range[4 + pair] = whi;
   }
   Frag<IO> kf[DH / 16];  // keys, or the second wave's values
   {
-    const void* p = second ? a.v : a.k;
-    const int64_t at = j * (second ? a.ldv : a.ldk) + (int64_t)hk * DH + 8 * h;
+    const void* p = SECOND ? a.v : a.k;
+    const int64_t at = j * (SECOND ? a.ldv : a.ldk) + (int64_t)hk * DH + 8 * h;
 #pragma unroll
     for (int s = 0; s < DH / 16; ++s) kf[s] = j < a.mask.T ? load_frag<IO>(p, at + 16 * s) : zero_frag<IO>();
     settle(kf);
   }
   __syncthreads();
-  int blo = min(min(range[0], range[1]), min(range[2], range[3]));
-  const int bhi = max(max(range[4], range[5]), max(range[6], range[7]));
-  if (bhi == 0) blo = 0;
+  const int end = __builtin_amdgcn_readfirstlane(max(max(range[4], range[5]), max(range[6], range[7])));
+  const int low = __builtin_amdgcn_readfirstlane(min(min(range[0], range[1]), min(range[2], range[3])));
+  const int blo = end == 0 ? 0 : low;
   const bool live = in_doc && lo < hi;
 
   f32x16_t acc[DH / 32];  // dv, or the second wave's dk
@@ -330,120 +324,154 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
     for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
   const float pre = a.mod.pre();
 
-  // the first four waves bring q, the others dout
-  Stage<IO, DH, kQ> stage;
-  const int thread = threadIdx.x % kThreads;
+  // the first waves bring q and the rows' lse, the second dout and δ
+  Stage<IO, DH, Q> stage;
   float s_stat = 0.f;
-  const int tiles = (bhi - blo + kQ - 1) / kQ, steps = tiles * G;
+  const int64_t ld = SECOND ? a.lddo : a.ldq;
+  const char* src = static_cast<const char*>(SECOND ? a.dout : a.q) + (int64_t)hk * G * DH * T::kElem;
+  const float* stats = (SECOND ? a.delta : a.lse) + (int64_t)hk * G * a.mask.T;
+  const int tiles = (end - blo + Q - 1) / Q, steps = tiles * G;
   const int per = (steps + a.pieces - 1) / a.pieces;
   const int first = min(piece * per, steps), last = min(first + per, steps);
   auto load = [&](int g, int row0) {
-    const int hq = hk * G + g;
-    const int64_t ld = second ? a.lddo : a.ldq;
-    stage.load(static_cast<const char*>(second ? a.dout : a.q) + (row0 * ld + (int64_t)hq * DH) * T::kElem, ld, bhi - row0,
-               thread);
-    if (threadIdx.x < 2 * kQ) {  // lse by the first kQ threads, δ by the next
-      const int row = row0 + threadIdx.x % kQ;
-      const float* p = threadIdx.x < kQ ? a.lse : a.delta;
-      s_stat = row < bhi ? p[(int64_t)hq * a.mask.T + row] : 0.f;
+    stage.load(src + (row0 * ld + g * DH) * T::kElem, ld, end - row0, thread);
+    if (thread < Q) s_stat = row0 + thread < end ? stats[(int64_t)g * a.mask.T + row0 + thread] : 0.f;
+  };
+  int g = first < last ? first / tiles : 0, row0 = blo + (first - g * tiles) * Q;  // the next tile's
+  if (first < last) load(g, row0);
+  const uint32_t base = lds_addr(lds);
+  float* ps = reinterpret_cast<float*>(lds + 5 * kTile) + pair * QB * 16 * kWave + lane * 4;
+  constexpr int kPs = 4 * QB * 16 * kWave;  // floats of one buffer of P
+  f32x16_t s[QB];                           // S and P, or the second wave's dP and dS
+  // LDS: three buffers of q (tile n is in use by the first waves while the second
+  // still need tile n - 1), two of dout
+  int cur = 0, prev = 0;  // q's buffers of tiles n and n - 1
+  auto dout_at = [&](int n) { return 3 * kTile + (n & 1) * kTile; };
+  // Tile n into its buffer, tile n + 1 on its way.
+  auto arrive = [&](int n) {
+    stage.store(lds + (SECOND ? dout_at(n) : cur * kTile), thread);
+    if (thread < Q) stat[cur][SECOND ? 1 : 0][thread] = SECOND ? s_stat : s_stat * kLog2e;
+    row0 += Q;
+    if (row0 >= end) {
+      row0 = blo;
+      ++g;
+    }
+    if (n + 1 < last) load(g, row0);
+    __syncthreads();
+  };
+  auto next = [&] {
+    prev = cur;
+    cur = cur == 2 ? 0 : cur + 1;
+  };
+  auto scores = [&](uint32_t ra) {
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
+      each<DH / 16>([&](auto m) { s[b] = mma(T::template row_frag<m>(ra, 32 * b * T::kRow), kf[m], s[b]); });
     }
   };
-  // (head, row) of the tile that is loaded next, and of this wave's
-  int lg = first < last ? first / tiles : 0, lrow = blo + (first - lg * tiles) * kQ;
-  int wg = lg, wrow = lrow;
-  if (first < last) load(lg, lrow);
-  int buf = 0, prev = 0;  // buffer of tile n, of tile n - 1
-  for (int n = first; n < last + 1; ++n) {
-    if (n < last) {
-      char* tq = lds + buf * 2 * kTile;
-      stage.store(second ? tq + kTile : tq, thread);
-      if (threadIdx.x < 2 * kQ) stat[buf][threadIdx.x / kQ][threadIdx.x % kQ] = threadIdx.x < kQ ? s_stat * kLog2e : s_stat;
-      lrow += kQ;
-      if (lrow >= bhi) {
-        lrow = blo;
-        ++lg;
+  auto sums = [&](uint32_t ca) {
+#pragma unroll
+    for (int b = 0; b < QB; ++b)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const Frag<IO> p = frag_of<IO>(s[b], m);
+        each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, (32 * b + 16 * m) * T::kRow), p, acc[d]); });
       }
-      if (n + 1 < last) load(lg, lrow);
+  };
+  if constexpr (!SECOND) {
+    for (int n = first; n < last; ++n) {
+      const int grow = g, r0 = row0, buf = cur;
+      arrive(n);
+      next();
+      if (r0 >= whi || r0 + Q <= wlo) continue;  // (the pair's two waves alike)
+      float* pw = ps + (n & 1) * kPs;
+      const bool partial = __any(live && (lo > r0 || hi < r0 + Q));
+      scores(T::row_addr(base + buf * kTile, c, h));
+      const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hk * G + grow] * kLog2e : 0.f;
+      const float d0 = (float)(r0 + 4 * h - j);
+#pragma unroll
+      for (int b = 0; b < QB; ++b) {
+        f32x16_t out;  // P, or P times the capping's derivative, for the second wave
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const float4 lse = *reinterpret_cast<const float4*>(&stat[buf][0][32 * b + 8 * r4 + 4 * h]);
+          const float lv[4] = {lse.x, lse.y, lse.z, lse.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 4 * r4 + e;
+            float sc, dcap = 1.f;
+            if constexpr (MOD != 0)
+              score<IO, MOD>(s[b][r], pre, a.mod, slope2, d0 + (float)(32 * b + 8 * r4 + e), sc, dcap);
+            else
+              sc = s[b][r] * pre;
+            s[b][r] = exp2_fast(sc - lv[e]);
+            if constexpr ((MOD & kCapped) != 0) out[r] = s[b][r] * dcap;
+          }
+        }
+        if (partial) {
+          int l0 = lo - r0 - 32 * b - 4 * h, h0 = hi - r0 - 32 * b - 4 * h;
+          keep_branch(l0, h0);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int k = 8 * (r >> 2) + (r & 3);
+            const bool seen = k >= l0 && k < h0;
+            s[b][r] = seen ? s[b][r] : 0.f;
+            if constexpr ((MOD & kCapped) != 0) out[r] = seen ? out[r] : 0.f;
+          }
+        }
+        if constexpr ((MOD & kCapped) == 0) out = s[b];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(pw + (4 * b + i) * kWave * 4) =
+              make_float4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+      }
+      sums(T::col_addr(base + dout_at(n), lane));
+    }
+    __syncthreads();  // the second waves' last tile
+  } else {
+    // dS of the tile before, whose first row is rp and whose P lies in `pr`
+    auto ds_of = [&](int rp, const float* pr) {
+      const bool partial = __any(live && (lo > rp || hi < rp + Q));
+#pragma unroll
+      for (int b = 0; b < QB; ++b) {
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const float4 del = *reinterpret_cast<const float4*>(&stat[prev][1][32 * b + 8 * r4 + 4 * h]);
+          const float4 p = *reinterpret_cast<const float4*>(pr + (4 * b + r4) * kWave * 4);
+          s[b][4 * r4] = p.x * (s[b][4 * r4] - del.x);
+          s[b][4 * r4 + 1] = p.y * (s[b][4 * r4 + 1] - del.y);
+          s[b][4 * r4 + 2] = p.z * (s[b][4 * r4 + 2] - del.z);
+          s[b][4 * r4 + 3] = p.w * (s[b][4 * r4 + 3] - del.w);
+        }
+        if (partial) {  // (0 times what is not finite)
+          int l0 = lo - rp - 32 * b - 4 * h, h0 = hi - rp - 32 * b - 4 * h;
+          keep_branch(l0, h0);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int k = 8 * (r >> 2) + (r & 3);
+            s[b][r] = k >= l0 && k < h0 ? s[b][r] : 0.f;
+          }
+        }
+      }
+    };
+    int rp = whi;  // (so that nothing is taken for the tile before the first)
+    for (int n = first; n < last; ++n) {
+      const int r0 = row0;
+      arrive(n);
+      if (rp < whi && rp + Q > wlo) {
+        ds_of(rp, ps + (~n & 1) * kPs);
+        sums(T::col_addr(base + prev * kTile, lane));
+      }
+      if (r0 < whi && r0 + Q > wlo) scores(T::row_addr(base + dout_at(n), c, h));
+      rp = r0;
+      next();
     }
     __syncthreads();
-    const int mine = second ? prev : buf, row0 = wrow;
-    const bool mine_now = second ? n > first : n < last;
-    float* ps = reinterpret_cast<float*>(lds + 6 * kTile) + (((second ? n - 1 : n) & 1) * 4 + pair) * 16 * kWave;
-    prev = buf;
-    buf = buf == 2 ? 0 : buf + 1;
-    if (!mine_now) continue;
-    const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hk * G + wg] * kLog2e : 0.f;
-    wrow += kQ;
-    if (wrow >= bhi) {
-      wrow = blo;
-      ++wg;
-    }
-    if (row0 >= whi || row0 + kQ <= wlo) continue;  // (the pair's two waves alike)
-    // the first wave reads the rows of q and the columns of dout, the second the reverse
-    const uint32_t tq = lds_addr(lds) + mine * 2 * kTile;
-    const uint32_t ra = T::row_addr(second ? tq + kTile : tq, c, h), ca = T::col_addr(second ? tq : tq + kTile, lane);
-    const bool partial = __any(live && (lo > row0 || hi < row0 + kQ));
-    f32x16_t s;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = 0.f;
-    each<DH / 16>([&](auto m) { s = mma(T::template row_frag<m>(ra, 0), kf[m], s); });
-    if (!second) {
-      const float d0 = (float)(row0 + 4 * h - j);
-      f32x16_t out;  // P, or P times the capping's derivative, for the second wave
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const float4 lse = *reinterpret_cast<const float4*>(&stat[mine][0][8 * r4 + 4 * h]);
-        const float lv[4] = {lse.x, lse.y, lse.z, lse.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * r4 + e;
-          float sc, dcap = 1.f;
-          if constexpr (MOD != 0)
-            score<IO, MOD>(s[r], pre, a.mod, slope2, d0 + (float)(8 * r4 + e), sc, dcap);
-          else
-            sc = s[r] * pre;
-          s[r] = exp2_fast(sc - lv[e]);
-          out[r] = s[r] * dcap;
-        }
-      }
-      if (partial) {
-        int l0 = lo - row0 - 4 * h, h0 = hi - row0 - 4 * h;
-        keep_branch(l0, h0);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int k = 8 * (r >> 2) + (r & 3);
-          const bool seen = k >= l0 && k < h0;
-          s[r] = seen ? s[r] : 0.f;
-          out[r] = seen ? out[r] : 0.f;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(ps + (i * kWave + lane) * 4) = make_float4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const float4 del = *reinterpret_cast<const float4*>(&stat[mine][1][8 * r4 + 4 * h]);
-        const float4 p = *reinterpret_cast<const float4*>(ps + (r4 * kWave + lane) * 4);
-        s[4 * r4] = p.x * (s[4 * r4] - del.x);
-        s[4 * r4 + 1] = p.y * (s[4 * r4 + 1] - del.y);
-        s[4 * r4 + 2] = p.z * (s[4 * r4 + 2] - del.z);
-        s[4 * r4 + 3] = p.w * (s[4 * r4 + 3] - del.w);
-      }
-      if (partial) {  // (0 times what is not finite)
-        int l0 = lo - row0 - 4 * h, h0 = hi - row0 - 4 * h;
-        keep_branch(l0, h0);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int k = 8 * (r >> 2) + (r & 3);
-          s[r] = k >= l0 && k < h0 ? s[r] : 0.f;
-        }
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const Frag<IO> p = frag_of<IO>(s, m);
-      each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, 16 * m * T::kRow), p, acc[d]); });
+    if (rp < whi && rp + Q > wlo) {
+      ds_of(rp, ps + (~last & 1) * kPs);
+      sums(T::col_addr(base + prev * kTile, lane));
     }
   }
   if (j >= a.mask.T) return;
@@ -453,17 +481,33 @@ __global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
   }
-  const float f = second ? a.mod.scale : 1.f;
+  const float f = SECOND ? a.mod.scale : 1.f;
   if (a.pieces > 1) {
     const int64_t all = (int64_t)a.mask.T * a.Hk * DH, at = ((int64_t)j * a.Hk + hk) * DH;
 #pragma unroll
-    for (int b = 0; b < DH / 32; ++b) store_block<kF32>(a.part, (2 * piece + (second ? 0 : 1)) * all + at, b, h, acc[b], f);
+    for (int b = 0; b < DH / 32; ++b) store_block<kF32>(a.part, (2 * piece + (SECOND ? 0 : 1)) * all + at, b, h, acc[b], f);
     return;
   }
   if (!in_doc && !a.fill) return;
-  const int64_t at = j * (second ? a.lddk : a.lddv) + (int64_t)hk * DH;
+  const int64_t at = j * (SECOND ? a.lddk : a.lddv) + (int64_t)hk * DH;
 #pragma unroll
-  for (int b = 0; b < DH / 32; ++b) store_block<IO>(second ? a.dk : a.dv, at, b, h, acc[b], f);
+  for (int b = 0; b < DH / 32; ++b) store_block<IO>(SECOND ? a.dk : a.dv, at, b, h, acc[b], f);
+}
+
+template <int IO, int DH, int MOD, int Q>
+__global__ __launch_bounds__(kKeyThreads, 2) void attn_bwd_keys_kernel(BwdArgs a) {
+  // three buffers of a row tile's q and two of its dout, then two of each pair's P
+  extern __shared__ __attribute__((aligned(512))) char lds[];
+  __shared__ int range[8];
+  __shared__ float stat[3][2][Q];  // [buffer][lse in log 2 units, δ][row]
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), thread = threadIdx.x % kThreads;
+  // The two kinds of wave run loops of their own (joined after each branch, the
+  // accumulators were copied between registers every step); both pass the same
+  // number of barriers.
+  if (wave < 4)
+    keys_wave<IO, DH, MOD, Q, false>(a, lds, range, stat, wave, lane, thread);
+  else
+    keys_wave<IO, DH, MOD, Q, true>(a, lds, range, stat, wave - 4, lane, thread);
 }
 
 // Adds up the pieces' partial sums: eight elements a thread, one key row of
@@ -494,11 +538,21 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_sum_kernel(BwdArgs a, int r
 
 static size_t delta_bytes(const mhc_attn_desc& d) { return ((size_t)d.Hq * (size_t)d.T * sizeof(float) + 255) / 256 * 256; }
 
+// Rows of the keys kernel's tiles: 64, which fill a CU's LDS with one workgroup
+// (bf16; fp32 takes 32), but 32 for heads of 64 on short documents, where three
+// smaller workgroups a CU hide their short loops' ends better.  Measured, 64 and
+// 32 rows: heads of 128, T = 8192 1.48 and 1.65 ms, documents of about 450 rows
+// 142 and 161 us; heads of 64, one document of 4096 rows 110 and 120 us,
+// documents of about 770 rows 47 and 40 us.
+static bool tall_tiles(const mhc_attn_desc& d) {
+  return d.io == MHC_BF16 && (d.Dh > 64 || d.T / (d.docs != nullptr ? d.n_docs : 1) >= 2048);
+}
+
 // Pieces of a key tile's steps: enough workgroups for two on every CU.
 static int pieces_of(const mhc_attn_desc& d) {
   const int64_t base = (d.T + kKeyRows - 1) / kKeyRows * d.Hk;
   int64_t n = (2 * device_cu_count() + base - 1) / base;
-  const int64_t steps = (d.T + kQ - 1) / kQ * (d.Hq / d.Hk);
+  const int64_t steps = (d.T + 31) / 32 * (d.Hq / d.Hk);
   if (n > (steps + 3) / 4) n = (steps + 3) / 4;  // at least four steps each
   if (n > kMaxPieces) n = kMaxPieces;
   return n < 1 ? 1 : (int)n;
@@ -543,6 +597,7 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
   const bool small = attn_short(d);
   const int per = small ? 32 : kRows;
   const dim3 rows((unsigned)((d.T + per - 1) / per * d.Hq));
+  const bool tall = tall_tiles(d);
   const dim3 keys((unsigned)((d.T + kKeyRows - 1) / kKeyRows * d.Hk * a.pieces));
   hipError_t err = hipErrorInvalidValue;
   dispatch_attn(d.io, d.Dh, d.softcap, d.slopes, [&](auto io_, auto dh_, auto mod_) {
@@ -557,7 +612,11 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
       MHC_LAUNCH((attn_bwd_rows_kernel<IO, DH, MOD>), rows, dim3(kThreads), 4 * kKeys * row, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return;
-    MHC_LAUNCH((attn_bwd_keys_kernel<IO, DH, MOD>), keys, dim3(kKeyThreads), 6 * kQ * row + 8 * 16 * kWave * 4, s, a);
+    [[maybe_unused]] constexpr int lds32 = 5 * 32 * row + 2 * 4 * 16 * kWave * 4, lds64 = 2 * lds32;
+    if constexpr (IO == kBF16)
+      if (tall) MHC_LAUNCH((attn_bwd_keys_kernel<IO, DH, MOD, 64>), keys, dim3(kKeyThreads), lds64, s, a);
+    if constexpr (IO == kF32 || DH == 64)
+      if (!tall) MHC_LAUNCH((attn_bwd_keys_kernel<IO, DH, MOD, 32>), keys, dim3(kKeyThreads), lds32, s, a);
     err = hipGetLastError();
     if (err != hipSuccess || a.pieces == 1) return;
     MHC_LAUNCH((attn_bwd_sum_kernel<IO>), dim3((unsigned)d.T), dim3(kThreads), 0, s, a, d.Hk * d.Dh);
