@@ -85,9 +85,11 @@ struct BwdRow {
 };
 
 // dq^T += K^T·dS^T of KB blocks of 32 keys from key0 on (`tk`, the values kTile
-// bytes further), masked to the lane's keys [lo, hi) where `partial`.
+// bytes further), masked to the lane's keys [lo, hi) where `partial`.  `rest`
+// adds up P (dP - δ), which over all keys is what δ, formed from o, is short of
+// Σ P·dP: o carries the roundings of the forward's probabilities.
 template <int IO, int DH, int KB, int MOD, int TILE>
-__device__ __forceinline__ void rows_step(f32x16_t (&acc)[DH / 32], const BwdRow<IO, DH>& row, uint32_t tk, int key0, int lo,
+__device__ __forceinline__ void rows_step(f32x16_t (&acc)[DH / 32], float& rest, const BwdRow<IO, DH>& row, uint32_t tk, int key0, int lo,
                                           int hi, bool partial, int i, float slope2, ScoreMod mod) {
   using T = Tile<IO, DH>;
   const int lane = threadIdx.x & (kWave - 1), c = lane & 31, h = lane >> 5;
@@ -111,9 +113,8 @@ __device__ __forceinline__ void rows_step(f32x16_t (&acc)[DH / 32], const BwdRow
         score<IO, MOD>(s[r], pre, mod, slope2, d0 - (float)k, sc, dcap);
       else
         sc = s[r] * pre;
-      float ds = exp2_fast(sc - row.lse2) * (dp[r] - row.delta);
-      if constexpr ((MOD & kCapped) != 0) ds *= dcap;
-      s[r] = ds;
+      s[r] = exp2_fast(sc - row.lse2) * (dp[r] - row.delta);
+      dp[r] = dcap;
     }
     if (partial) {
       int l0 = lo - key0 - 32 * b - 4 * h, h0 = hi - key0 - 32 * b - 4 * h;
@@ -124,6 +125,13 @@ __device__ __forceinline__ void rows_step(f32x16_t (&acc)[DH / 32], const BwdRow
         s[r] = k >= l0 && k < h0 ? s[r] : 0.f;
       }
     }
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      sum += s[r];
+      if constexpr ((MOD & kCapped) != 0) s[r] *= dp[r];
+    }
+    rest += sum;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const Frag<IO> ds = frag_of<IO>(s, n);
@@ -162,12 +170,12 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
 
   BwdRow<IO, DH> row;
   row.load(a, i, hq, h, live);
-  if (i < a.mask.T && h == 0) a.delta[(int64_t)hq * a.mask.T + i] = live ? row.delta : 0.f;
 
   const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
   const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
   Stage<IO, DH, kKeys> sk, sv;
   const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hq] * kLog2e : 0.f;
+  float rest = 0.f;
   f32x16_t acc[DH / 32];
 #pragma unroll
   for (int b = 0; b < DH / 32; ++b)
@@ -189,8 +197,10 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
     __syncthreads();
     if (key0 >= whi || next <= wlo) continue;
     const bool partial = __any(live && (lo > key0 || hi < next));
-    rows_step<IO, DH, kKeys / 32, MOD, kTile>(acc, row, lds_addr(tk), key0, lo, hi, partial, i, slope2, a.mod);
+    rows_step<IO, DH, kKeys / 32, MOD, kTile>(acc, rest, row, lds_addr(tk), key0, lo, hi, partial, i, slope2, a.mod);
   }
+  rest += other_half(rest);
+  if (i < a.mask.T && h == 0) a.delta[(int64_t)hq * a.mask.T + i] = live ? row.delta + rest : 0.f;
   if (i >= a.mask.T || (!in_doc && !a.fill)) return;
 #pragma unroll
   for (int b = 0; b < DH / 32; ++b) {
@@ -209,6 +219,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_s
   using T = Tile<IO, DH>;
   constexpr int kTile = 32 * T::kRow;
   extern __shared__ __attribute__((aligned(512))) char lds[];
+  __shared__ float rests[4][32];
   const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   const int G = a.Hq / a.Hk;
   const int nt = (a.mask.T + 31) / 32;
@@ -222,12 +233,12 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_s
   const bool live = in_doc && lo < hi;
   BwdRow<IO, DH> row;
   row.load(a, i, hq, h, live);
-  if (i < a.mask.T && wave == 0 && h == 0) a.delta[(int64_t)hq * a.mask.T + i] = live ? row.delta : 0.f;
 
   const char* kb = static_cast<const char*>(a.k) + (int64_t)hk * DH * T::kElem;
   const char* vb = static_cast<const char*>(a.v) + (int64_t)hk * DH * T::kElem;
   Stage<IO, DH, 32, kWave> sk, sv;
   const float slope2 = (MOD & kSloped) != 0 ? a.slopes[hq] * kLog2e : 0.f;
+  float rest = 0.f;
   f32x16_t acc[DH / 32];
 #pragma unroll
   for (int b = 0; b < DH / 32; ++b)
@@ -250,7 +261,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_s
     }
     wave_lds_fence();
     const bool partial = __any(live && (lo > key0 || hi < key0 + 32));
-    rows_step<IO, DH, 1, MOD, kTile>(acc, row, lds_addr(tk), key0, lo, hi, partial, i, slope2, a.mod);
+    rows_step<IO, DH, 1, MOD, kTile>(acc, rest, row, lds_addr(tk), key0, lo, hi, partial, i, slope2, a.mod);
     wave_lds_fence();
   }
   if (!live) {
@@ -259,7 +270,11 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_s
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[b][r] = 0.f;
   }
-  __syncthreads();  // every wave is done with its tiles
+  rest += other_half(rest);
+  if (lane < 32) rests[wave][c] = rest;
+  __syncthreads();  // (every wave is done with its tiles, too)
+  if (i < a.mask.T && wave == 0 && h == 0)
+    a.delta[(int64_t)hq * a.mask.T + i] = live ? row.delta + ((rests[0][c] + rests[1][c]) + (rests[2][c] + rests[3][c])) : 0.f;
   const f32x16_t sum = sum_waves<DH>(lds, wave, lane, acc, a.mod.scale);
   if (wave >= DH / 32 || i >= a.mask.T || (!in_doc && !a.fill)) return;
   store_block<IO>(a.dq, i * a.lddq + (int64_t)hq * DH, wave, h, sum, 1.f);
