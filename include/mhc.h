@@ -350,7 +350,9 @@ typedef struct mhc_attn_desc {
 
 /* o_i = Σ_j softmax_j(s_ij) v_j, and for the backward lse[Hq][T] (fp32,
  * natural log; NULL to skip) and, bf16 only, o_rest[T][Hq][Dh] (one byte an
- * element: the next eight bits of o after its rounding; NULL to skip). */
+ * element: the next eight bits of o after its rounding; NULL to skip).
+ * Infinities and NaN in k and v reach the rows that see their key and no
+ * others, those in q their own row. */
 mhc_status mhc_attn(const mhc_attn_desc* desc, const void* q, const void* k, const void* v, void* o, float* lse,
                     void* o_rest, hipStream_t stream);
 
@@ -361,7 +363,10 @@ size_t mhc_attn_bwd_workspace_bytes(const mhc_attn_desc* desc);
  * dk, dv [T][Hk][Dh] summed over the query heads that share a key head.  slopes
  * are constants.  Rows of no document as in the forward.  Without o_rest (NULL)
  * the rows' do·o is formed from the rounded o alone; that rounding is then the
- * largest error of dq and dk where a row's weight lies on few keys. */
+ * largest error of dq and dk where a row's weight lies on few keys.
+ * Infinities and NaN in a document's rows may make NaN of gradients of rows and
+ * keys up to 128 places from them that do not see them; those in rows of no
+ * document reach nothing. */
 mhc_status mhc_attn_bwd(const mhc_attn_desc* desc, const void* dout, const void* q, const void* k, const void* v,
                         const void* o, const float* lse, const void* o_rest, void* dq, void* dk, void* dv,
                         void* workspace, size_t workspace_bytes, hipStream_t stream);
@@ -378,8 +383,9 @@ mhc_status mhc_attn_bwd(const mhc_attn_desc* desc, const void* dout, const void*
  * j ≤ p, of these with window > 0 only p - j < window, or else with prefix
  * (device, int32[n_seqs]) also the keys j < prefix[s].  A row that sees no key
  * gets zeros; a row whose sequence's keys lie in a page outside the cache gets
- * NaN.  Rows of no sequence as rows of no document above.  Scores, Dh, strides
- * as above; num_pages·page_size < 2^31. */
+ * NaN.  Rows of no sequence as rows of no document above (with n_seqs 0 nothing
+ * is written at all).  Scores, Dh, strides, infinities and NaN as above;
+ * num_pages·page_size < 2^31. */
 typedef struct mhc_paged_desc {
   int64_t T;
   int32_t n_seqs;

@@ -202,6 +202,38 @@ __device__ __forceinline__ void each(F&& f) {
   }
 }
 
+// Whether one of N chunks holds an infinity or NaN: the largest magnitude, as
+// bit patterns, reaches infinity's.
+template <int IO, int N>
+__device__ __forceinline__ bool any_not_finite(const u32x4_t (&w)[N]) {
+  typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+  if constexpr (IO == kBF16) {
+    u16x2_t m{0, 0};
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[n][e] & 0x7fff7fffu));
+    return m.x >= 0x7f80u || m.y >= 0x7f80u;
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = max(m, w[n][e] & 0x7fffffffu);
+    return m >= 0x7f800000u;
+  }
+}
+// A chunk with zeros in their place.
+template <int IO>
+__device__ __forceinline__ u32x4_t finite_part(u32x4_t w) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const bool top = (w[e] & 0x7f800000u) == 0x7f800000u, low = IO == kBF16 && (w[e] & 0x7f80u) == 0x7f80u;
+    w[e] = IO == kBF16 ? (top ? 0u : w[e] & 0xffff0000u) | (low ? 0u : w[e] & 0xffffu) : top ? 0u : w[e];
+  }
+  return w;
+}
+
 // Staging of R head rows by NT threads: global memory to registers, then
 // registers to LDS, so that the next tile is on its way while this one is
 // used.  Thread i takes chunk i mod C of rows i/C, i/C + NT/C, ...
@@ -230,6 +262,14 @@ struct Stage {
 #pragma unroll
     for (int n = 0; n < kN; ++n)
       *reinterpret_cast<u32x4_t*>(t + T::at(thread / T::kChunks + n * kStep, thread % T::kChunks)) = w[n];
+  }
+  // After store: zeros over infinities and NaN; true if the thread has any.
+  __device__ __forceinline__ bool store_finite(char* t, int thread = threadIdx.x) const {
+    if (__builtin_expect(!any_not_finite<IO>(w), 1)) return false;
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+      *reinterpret_cast<u32x4_t*>(t + T::at(thread / T::kChunks + n * kStep, thread % T::kChunks)) = finite_part<IO>(w[n]);
+    return true;
   }
 };
 
@@ -530,6 +570,49 @@ __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH
 // LDS bytes of join_waves / sum_waves.
 template <int DH>
 constexpr int wave_states_bytes() { return 4 * (DH / 32) * 16 * kWave * 4; }
+
+// Values go into masked tiles without their infinities and NaN: in the product
+// 0 · NaN would hand them to the rows that do not see their key as well.  This
+// adds those of the keys first..end - 1 that the lane's row does see, key by
+// key from global memory.  `row(j)`: address of key j's value row.
+template <int IO, int DH, typename F>
+__device__ __forceinline__ void add_not_finite(RowState<DH>& st, int first, int end, int h, F&& row) {
+#pragma unroll 1
+  for (int j = first; j < end; ++j) {
+    const char* v = row(j);
+#pragma unroll
+    for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[4];
+        const int at = 32 * b + 8 * i + 4 * h;
+        if constexpr (IO == kBF16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(v + 2 * at);
+          x[0] = __uint_as_float(w.x << 16);
+          x[1] = __uint_as_float(w.x & 0xffff0000u);
+          x[2] = __uint_as_float(w.y << 16);
+          x[3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+          const float4 w = *reinterpret_cast<const float4*>(v + 4 * at);
+          x[0] = w.x;
+          x[1] = w.y;
+          x[2] = w.z;
+          x[3] = w.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          st.o[b][4 * i + e] += fabsf(x[e]) < __builtin_inff() ? 0.f : x[e];
+      }
+  }
+}
+
+// Keys that every lane with lo < hi sees, for ranges that do not go back from
+// one lane to the next: [ilo, ihi), all keys if there is no such lane.
+__device__ __forceinline__ void common_range(int lo, int hi, int& ilo, int& ihi) {
+  const uint64_t live = __ballot(lo < hi);
+  ilo = live == 0 ? 0 : __builtin_amdgcn_readlane(lo, 31 - __clz((int)(uint32_t)live));
+  ihi = live == 0 ? 0x7fffffff : __builtin_amdgcn_readlane(hi, __ffs((int)(uint32_t)live) - 1);
+}
 
 // Sums four waves' accumulators x[block] (scaled by f) for the same 32 columns:
 // wave w < DH/32 returns block w of the sum.  `lds`: wave_states_bytes, free

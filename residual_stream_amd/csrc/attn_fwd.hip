@@ -40,7 +40,8 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
   extern __shared__ __attribute__((aligned(512))) char lds[];  // two buffers of a key and a value tile
-  __shared__ int range[8];
+  __shared__ int range[16];
+  __shared__ int not_finite;  // some value of a masked tile is not
   const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   // Tiles from the last (under a causal mask the longest) down; the heads of a
   // tile vary fastest, key head first: consecutive workgroups go to the eight
@@ -60,7 +61,16 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
     range[wave] = whi > 0 ? wlo : 0x7fffffff;
     range[4 + wave] = whi;
   }
+  int ilo, ihi;
+  common_range(lo, hi, ilo, ihi);
+  if (lane == 0) {
+    range[8 + wave] = ilo;
+    range[12 + wave] = ihi;
+  }
+  if (threadIdx.x == 0) not_finite = 0;
   __syncthreads();
+  ilo = max(max(range[8], range[9]), max(range[10], range[11]));
+  ihi = min(min(range[12], range[13]), min(range[14], range[15]));
   int blo = min(min(range[0], range[1]), min(range[2], range[3]));
   const int bhi = max(max(range[4], range[5]), max(range[6], range[7]));
   if (bhi == 0) blo = 0;
@@ -86,19 +96,23 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
   for (int key0 = blo; key0 < bhi; key0 += kKeys, buf ^= 1) {
     char* tk = lds + buf * 2 * kTile;
     char* tv = tk + kTile;
-    sk.store(tk);
-    sv.store(tv);
     const int next = key0 + kKeys;
-    if (next < bhi) {
-      sk.load(kb + next * a.ldk * T::kElem, a.ldk, bhi - next);
-      sv.load(vb + next * a.ldv * T::kElem, a.ldv, bhi - next);
-    }
+    sk.store(tk);
+    if (next < bhi) sk.load(kb + next * a.ldk * T::kElem, a.ldk, bhi - next);
+    sv.store(tv);
+    if ((key0 < ilo || next > ihi) && sv.store_finite(tv)) not_finite = 1;
+    if (next < bhi) sv.load(vb + next * a.ldv * T::kElem, a.ldv, bhi - next);
     __syncthreads();
     if (key0 < whi && next > wlo) {
       const bool partial = __any(live && (lo > key0 || hi < next));
       attend<IO, DH, kKeys / 32, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, lo, hi, partial, i, slope2, a.mod);
     }
   }
+  if (__builtin_expect(not_finite, 0))
+    for (int key0 = blo; key0 < bhi; key0 += kKeys)
+      if (key0 < ilo || key0 + kKeys > ihi)
+        add_not_finite<IO, DH>(st, max(lo, key0), min(hi, key0 + kKeys), h,
+                               [&](int j) { return vb + j * a.ldv * T::kElem; });
   if (i >= a.mask.T || (!in_doc && !a.fill)) return;
   const float l = st.l + other_half(st.l);
   const float inv = !live || l == 0.f ? 0.f : 1.f / l;
@@ -149,24 +163,30 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_short_
   st.init();
   char* tk = lds + wave * 2 * kTile;
   char* tv = tk + kTile;
+  bool not_finite = false;
   int key0 = wlo + wave * 32;
   if (key0 < whi) {
     sk.load(kb + key0 * a.ldk * T::kElem, a.ldk, whi - key0, lane);
     sv.load(vb + key0 * a.ldv * T::kElem, a.ldv, whi - key0, lane);
   }
   for (; key0 < whi; key0 += 128) {
+    const bool partial = __any(live && (lo > key0 || hi < key0 + 32));
     sk.store(tk, lane);
     sv.store(tv, lane);
+    if (partial) not_finite |= sv.store_finite(tv, lane);
     const int next = key0 + 128;
     if (next < whi) {
       sk.load(kb + next * a.ldk * T::kElem, a.ldk, whi - next, lane);
       sv.load(vb + next * a.ldv * T::kElem, a.ldv, whi - next, lane);
     }
     wave_lds_fence();
-    const bool partial = __any(live && (lo > key0 || hi < key0 + 32));
     attend<IO, DH, 1, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, lo, hi, partial, i, slope2, a.mod);
     wave_lds_fence();
   }
+  if (__builtin_expect(__any(not_finite), 0))
+    for (key0 = wlo + wave * 32; key0 < whi; key0 += 128)
+      if (__any(live && (lo > key0 || hi < key0 + 32)))
+        add_not_finite<IO, DH>(st, max(lo, key0), min(hi, key0 + 32), h, [&](int j) { return vb + j * a.ldv * T::kElem; });
   if (!live) st.init();
   float m, l;
   const f32x16_t sum = join_waves<DH>(lds, stat, wave, lane, st, m, l);

@@ -109,8 +109,7 @@ __device__ __forceinline__ Row row_of(const PagedArgs& a, int s, const Seq& q, i
 
 // Staging of R cache rows by NT threads: as Stage, with each row's entry of
 // the page table read one tile ahead of its load (and not looked at before, so
-// that nothing waits for it).  Rows past `last` re-read it (they are masked,
-// and what is read is finite wherever the last row's keys and values are).
+// that nothing waits for it).  Rows past `last` re-read it (they are masked).
 template <int IO, int DH, int R, int NT>
 struct PagedStage {
   using T = Tile<IO, DH>;
@@ -118,16 +117,23 @@ struct PagedStage {
   static constexpr int kStep = NT / T::kChunks;
   static_assert(R * T::kChunks % NT == 0 && NT % T::kChunks == 0, "whole passes");
   u32x4_t k[kN], v[kN];
+  int64_t at[kN];
   int entry[kN];
 
+  // Address of key r's value row, for a key whose page is in the cache.
+  __device__ static __forceinline__ const char* value_row(const PagedArgs& a, const int32_t* table, int hk, int r) {
+    const int p = a.by_page(r);
+    int e = table[p];
+    if ((unsigned)e >= (unsigned)a.num_pages) e = 0;  // (the rows come out as NaN)
+    return static_cast<const char*>(a.vc) + (((int64_t)e * a.page_size + (r - p * a.page_size)) * a.Hk + hk) * T::kRow;
+  }
   __device__ __forceinline__ void lookup(const PagedArgs& a, const int32_t* table, int thread, int row0, int last) {
 #pragma unroll
     for (int n = 0; n < kN; ++n) entry[n] = table[a.by_page(min(row0 + thread / T::kChunks + n * kStep, last))];
   }
-  __device__ __forceinline__ void load(const PagedArgs& a, int hk, int thread, int row0, int last, bool& bad) {
+  __device__ __forceinline__ void load_k(const PagedArgs& a, int hk, int thread, int row0, int last, bool& bad) {
     const int64_t row = (int64_t)a.Hk * T::kRow;
     const int64_t in = (int64_t)hk * T::kRow + (thread % T::kChunks) * 16;
-    int64_t at[kN];
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       const int r = min(row0 + thread / T::kChunks + n * kStep, last);
@@ -140,16 +146,27 @@ struct PagedStage {
     }
 #pragma unroll
     for (int n = 0; n < kN; ++n) k[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.kc) + at[n]);
+  }
+  __device__ __forceinline__ void load_v(const PagedArgs& a) {  // (after load_k: the same places)
 #pragma unroll
     for (int n = 0; n < kN; ++n) v[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.vc) + at[n]);
   }
-  __device__ __forceinline__ void store(char* tk, char* tv, int thread) const {
+  __device__ __forceinline__ void load(const PagedArgs& a, int hk, int thread, int row0, int last, bool& bad) {
+    load_k(a, hk, thread, row0, last, bad);
+    load_v(a);
+  }
+  __device__ static __forceinline__ void store(char* t, const u32x4_t (&w)[kN], int thread) {
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      const int at = T::at(thread / T::kChunks + n * kStep, thread % T::kChunks);
-      *reinterpret_cast<u32x4_t*>(tk + at) = k[n];
-      *reinterpret_cast<u32x4_t*>(tv + at) = v[n];
-    }
+    for (int n = 0; n < kN; ++n)
+      *reinterpret_cast<u32x4_t*>(t + T::at(thread / T::kChunks + n * kStep, thread % T::kChunks)) = w[n];
+  }
+  // After store: zeros over the values' infinities and NaN; true if the thread has any.
+  __device__ __forceinline__ bool store_finite(char* tv, int thread) const {
+    if (__builtin_expect(!any_not_finite<IO>(v), 1)) return false;
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+      *reinterpret_cast<u32x4_t*>(tv + T::at(thread / T::kChunks + n * kStep, thread % T::kChunks)) = finite_part<IO>(v[n]);
+    return true;
   }
 };
 
@@ -232,6 +249,10 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
   char* tv = tk + kTile;
   PagedStage<IO, DH, kFewKeys, kWave> sg;
   const int32_t* table = a.pages + (int64_t)s * a.max_pages;
+  auto masked = [&](int key0) {
+    return __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kFewKeys)) || key0 + kFewKeys > hi;
+  };
+  bool not_finite = false;
   int key0 = lo + wave * kFewKeys;
   constexpr int kAll = 4 * kFewKeys;
   if (key0 < hi) {
@@ -240,14 +261,21 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
     if (key0 + kAll < hi) sg.lookup(a, table, lane, key0 + kAll, hi - 1);
   }
   for (; key0 < hi; key0 += kAll) {
-    sg.store(tk, tv, lane);
+    const bool partial = masked(key0);
+    sg.store(tk, sg.k, lane);
+    sg.store(tv, sg.v, lane);
+    if (partial) not_finite |= sg.store_finite(tv, lane);
     if (key0 + kAll < hi) sg.load(a, hk, lane, key0 + kAll, hi - 1, bad);
     if (key0 + 2 * kAll < hi) sg.lookup(a, table, lane, key0 + 2 * kAll, hi - 1);
     wave_lds_fence();
-    const bool partial = __any(r.lo < r.hi && (r.lo > key0 || r.hi < key0 + kFewKeys)) || key0 + kFewKeys > hi;
     attend<IO, DH, 1, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, r.lo, min(r.hi, hi), partial, r.pos, slope2, a.mod);
     wave_lds_fence();
   }
+  if (__builtin_expect(__any(not_finite), 0))
+    for (key0 = lo + wave * kFewKeys; key0 < hi; key0 += kAll)
+      if (masked(key0))
+        add_not_finite<IO, DH>(st, max(r.lo, key0), min(min(r.hi, hi), key0 + kFewKeys), h,
+                               [&](int j) { return sg.value_row(a, table, hk, j); });
   if (__any(bad) && lane == 0) any_bad = 1;
   if (r.lo >= r.hi) st.init();  // (unmasked tiles were not for this row)
   float m, l;
@@ -270,8 +298,9 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
   using T = Tile<IO, DH>;
   constexpr int kTile = kKeys * T::kRow;
   extern __shared__ __attribute__((aligned(512))) char lds[];
-  __shared__ int range[8];
+  __shared__ int range[16];
   __shared__ int any_bad;
+  __shared__ int not_finite;  // some value of a masked tile is not
   fill_rest<IO, DH>(a);
   const int lane = threadIdx.x & (kWave - 1), wave = wave_id(), c = lane & 31, h = lane >> 5;
   const int hk = blockIdx.x % a.Hk;
@@ -289,12 +318,21 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
     range[wave] = whi > 0 ? wlo : 0x7fffffff;
     range[4 + wave] = whi;
   }
-  if (threadIdx.x == 0) any_bad = 0;
+  int ilo, ihi;
+  common_range(r.lo, r.hi, ilo, ihi);
+  if (lane == 0) {
+    range[8 + wave] = ilo;
+    range[12 + wave] = ihi;
+  }
+  if (threadIdx.x == 0) any_bad = not_finite = 0;
   __syncthreads();
+  ilo = max(max(range[8], range[9]), max(range[10], range[11]));
+  ihi = min(min(range[12], range[13]), min(range[14], range[15]));
   int blo = min(min(range[0], range[1]), min(range[2], range[3]));
   int bhi = max(max(range[4], range[5]), max(range[6], range[7]));
   if (bhi == 0) blo = 0;
   split_range(a.splits, sp, kKeys, blo, bhi);
+  ihi = min(ihi, bhi);
 
   Frag<IO> qf[DH / 16];
   load_q<IO, DH>(a, r, h, qf);
@@ -314,8 +352,11 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
   for (int key0 = blo; key0 < bhi; key0 += kKeys, buf ^= 1) {
     char* tk = lds + buf * 2 * kTile;
     char* tv = tk + kTile;
-    sg.store(tk, tv, threadIdx.x);
-    if (key0 + kKeys < bhi) sg.load(a, hk, threadIdx.x, key0 + kKeys, bhi - 1, bad);
+    sg.store(tk, sg.k, threadIdx.x);
+    if (key0 + kKeys < bhi) sg.load_k(a, hk, threadIdx.x, key0 + kKeys, bhi - 1, bad);
+    sg.store(tv, sg.v, threadIdx.x);
+    if ((key0 < ilo || key0 + kKeys > ihi) && sg.store_finite(tv, threadIdx.x)) not_finite = 1;
+    if (key0 + kKeys < bhi) sg.load_v(a);
     if (key0 + 2 * kKeys < bhi) sg.lookup(a, table, threadIdx.x, key0 + 2 * kKeys, bhi - 1);
     __syncthreads();
     if (key0 < whi && key0 + kKeys > wlo) {
@@ -323,6 +364,11 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
       attend<IO, DH, kKeys / 32, MOD>(st, qf, lds_addr(tk), lds_addr(tv), key0, r.lo, min(r.hi, bhi), partial, r.pos, slope2, a.mod);
     }
   }
+  if (__builtin_expect(not_finite, 0))
+    for (int key0 = blo; key0 < bhi; key0 += kKeys)
+      if (key0 < ilo || key0 + kKeys > ihi)
+        add_not_finite<IO, DH>(st, max(r.lo, key0), min(min(r.hi, bhi), key0 + kKeys), h,
+                               [&](int j) { return sg.value_row(a, table, hk, j); });
   if (__any(bad) && lane == 0) any_bad = 1;
   __syncthreads();
   if (!r.real) return;

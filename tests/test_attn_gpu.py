@@ -259,3 +259,29 @@ def test_graph_replays_match_eager(Hq, Hk):
         torch.cuda.synchronize()
         for a, b in zip(got, ref):
             same(f"replay {rep}", a, b)
+
+
+@pytest.mark.parametrize("io,Dh", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (160, 40)])
+@pytest.mark.parametrize("masks", [dict(docs=[0, 70, 75, 200]), dict(window=40), dict(prefix=[90])], ids=["docs", "window", "prefix"])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(io, Dh, Hq, Hk, masks):
+    """In a column of v: that column of those rows; in k: those rows; elsewhere what finite inputs give."""
+    (q, k, v, _), kw, ok, dist, ref = _case(io, 200, Hq, Hk, Dh, seed=11, **masks)
+    clean_k, clean_v = host(k), host(v)
+    inf, nan = float("inf"), float("nan")
+    places = [(60, 3, inf), (72, Dh - 1, nan), (101, 0, -inf), (199, 31, nan)]
+    for j, d, x in places:
+        v[j, :, d] = x
+    k[130, :, 5] = nan
+    some = [0, Hq // Hk, Hq - 1]  # heads that the oracle looks at
+    of = [h * Hk // Hq for h in some]
+    o = host(attn.mhc_attn(q, k, v, **kw)[0])[:, some]
+    ro, _, eo = O.attention(host(q)[:, some], clean_k[:, of], clean_v[:, of], ok, dist, **ref)
+    hit = np.repeat(ok[:, 130][:, None], Dh, 1)
+    for j, d, _ in places:
+        hit[:, d] |= ok[:, j]
+    hit = np.broadcast_to(hit[:, None], o.shape)
+    assert not np.isfinite(o[hit]).any()
+    close("o", np.where(hit, ro, o), ro, eo)
+    only = ok[:, 60] & ~ok[:, 130]
+    assert (o[only][:, :, 3] == inf).all()

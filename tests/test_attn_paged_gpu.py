@@ -224,3 +224,30 @@ def test_graph_replays_match_eager(new):
         torch.cuda.synchronize()
         got = out.clone()
         same(f"replay {rep}", got, call())
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("new,Hq,Hk,Dh", [(9, 4, 2, 128), (70, 8, 2, 64), (90, 4, 2, 128)])
+@pytest.mark.parametrize("kv", [97, 1500])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(io, new, Hq, Hk, Dh, kv):
+    page = 16
+    q, kc, vc, table = _paged(io, [kv], [new], Hq, Hk, Dh, page, seed=5)
+    t = host(table).astype(int)[0]
+    rows = lambda c: host(c)[t].reshape(-1, Hk, Dh)[:kv]  # noqa: E731
+    clean = rows(kc), rows(vc)
+    first, last = kv - new, kv - 1
+    places = [(first + 2, 1, float("inf")), (first + 5, Dh - 2, float("nan")), (last, 40, float("-inf"))]
+    for j, d, x in places:
+        vc[t[j // page], j % page, :, d] = x
+    kc[t[(last - 1) // page], (last - 1) % page, :, 0] = float("nan")
+    o = host(attn.mhc_attn_paged(q, kc, vc, table, ints([kv]), cu_q=ints([0, new]), max_q=new))
+    p = kv - new + np.arange(new)
+    ok = np.arange(kv)[None] <= p[:, None]
+    ref, _, bound = O.attention(host(q), *clean, ok, np.abs(p[:, None] - np.arange(kv)[None]).astype(float), io=io,
+                                scale=Dh ** -0.5, softcap=0.0, slopes=None)
+    hit = np.repeat(ok[:, last - 1][:, None], Dh, 1)
+    for j, d, _ in places:
+        hit[:, d] |= ok[:, j]
+    hit = np.broadcast_to(hit[:, None], o.shape)
+    assert not np.isfinite(o[hit]).any()
+    close("o", np.where(hit, ref, o), ref, bound + 2.0 ** -20 * np.abs(ref).max())
