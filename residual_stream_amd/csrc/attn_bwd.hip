@@ -87,7 +87,8 @@ struct BwdRow {
 // dq^T += K^T·dS^T of KB blocks of 32 keys from key0 on (`tk`, the values kTile
 // bytes further), masked to the lane's keys [lo, hi) where `partial`.  `rest`
 // adds up P (dP - δ), which over all keys is what δ, formed from o, is short of
-// Σ P·dP: o carries the roundings of the forward's probabilities.
+// Σ P·dP: o carries the roundings of the forward's probabilities.  bf16: dS of
+// masked tiles goes in to twice the bits, as the forward's probabilities do.
 template <int IO, int DH, int KB, int MOD, int TILE>
 __device__ __forceinline__ void rows_step(f32x16_t (&acc)[DH / 32], float& rest, const BwdRow<IO, DH>& row, uint32_t tk, int key0, int lo,
                                           int hi, bool partial, int i, float slope2, ScoreMod mod) {
@@ -137,6 +138,13 @@ __device__ __forceinline__ void rows_step(f32x16_t (&acc)[DH / 32], float& rest,
       const Frag<IO> ds = frag_of<IO>(s, n);
       each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, (32 * b + 16 * n) * T::kRow), ds, acc[d]); });
     }
+    if constexpr (IO == kBF16)
+      if (partial)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const Frag<IO> ds = rest_frag(s, n);
+          each<DH / 32>([&](auto d) { acc[d] = mma(T::template col_frag<d>(ca, (32 * b + 16 * n) * T::kRow), ds, acc[d]); });
+        }
   }
 }
 

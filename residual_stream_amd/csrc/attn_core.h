@@ -109,6 +109,18 @@ __device__ __forceinline__ Frag<IO> frag_of(const f32x16_t& x, int half) {
   return f;
 }
 
+// bf16: the operand formed from what that rounding leaves.
+__device__ __forceinline__ Frag<kBF16> rest_frag(const f32x16_t& x, int half) {
+  Frag<kBF16> f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a = x[8 * half + 2 * e], b = x[8 * half + 2 * e + 1];
+    const uint32_t p = pack_bf16x2(a, b);
+    f.w[e] = pack_bf16x2(a - __uint_as_float(p << 16), b - __uint_as_float(p & 0xffff0000u));
+  }
+  return f;
+}
+
 // A tile of head rows in LDS, 16-byte chunks.  Chunk c of row r lies at place
 // c ^ swz(r) of the row.  Sixteen consecutive rows put one chunk on all 64
 // banks (reads along the rows), and four consecutive rows, a multiple of four
@@ -496,7 +508,10 @@ struct RowState {
 // `key0`: index of the tile's first key; `pos`: the row's own index.
 // The maximum is let lag by up to 2⁶: a new maximum rescales the output only
 // when it would overflow that margin (p stays ≤ 64, exact in fp32 sums, and
-// bf16 keeps its relative precision at any scale).
+// bf16 keeps its relative precision at any scale).  bf16: a probability is
+// rounded for the second product, which averages out over many keys; a masked
+// tile's, which may be all that a row has, go in to twice the bits, by a second
+// pass over their rests.
 template <int IO, int DH, int KB, int MOD>
 __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH / 16], uint32_t tk, uint32_t tv,
                                        int key0, int lo, int hi, bool partial, int pos, float slope2, ScoreMod mod) {
@@ -565,6 +580,15 @@ __device__ __forceinline__ void attend(RowState<DH>& st, const Frag<IO> (&qf)[DH
       const Frag<IO> p = frag_of<IO>(s[b], i);
       each<DH / 32>([&](auto d) { st.o[d] = mma(T::template col_frag<d>(va, (32 * b + 16 * i) * T::kRow), p, st.o[d]); });
     }
+  if constexpr (IO == kBF16)
+    if (partial)
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Frag<IO> p = rest_frag(s[b], i);
+          each<DH / 32>([&](auto d) { st.o[d] = mma(T::template col_frag<d>(va, (32 * b + 16 * i) * T::kRow), p, st.o[d]); });
+        }
 }
 
 // LDS bytes of join_waves / sum_waves.
