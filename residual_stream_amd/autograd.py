@@ -406,6 +406,11 @@ class MHCAttention(torch.nn.Module):
 
     Parameters: qkv[(heads + 2·key_heads)·head_dim, hidden] and out[hidden,
     heads·head_dim] in `dtype`, q_weight and k_weight [head_dim] in fp32.
+
+    A pass can be captured in a HIP graph, with the batch's tensors updated in
+    place between replays.  As for any torch module, let go of eager passes'
+    outputs before a backward is captured: a gradient accumulator that an eager
+    graph of the same parameters keeps alive belongs to the eager stream.
     """
 
     def __init__(self, hidden: int, heads: int, key_heads: int, head_dim: int, *, rotated: int | None = None,

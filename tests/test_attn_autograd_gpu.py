@@ -175,3 +175,61 @@ def test_refusals():
         CacheBatch.step(pages, [10], [7], 16)
     with pytest.raises(ValueError, match="evenly"):
         MHCAttention(64, 3, 2, 64)
+
+
+def _captured(step):
+    """`step` in a graph, after one eager pass on a stream of its own."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    return g, out
+
+
+def test_a_captured_training_pass_replays_like_the_eager_one():
+    m = _layer(hidden=256, softcap=20.0)
+    m.batch = AttnBatch.packed([70, 1, 58])
+    x, gy = (torch.randn(129, 256, device="cuda") for _ in range(2))
+    x.requires_grad_()
+    step = lambda: torch.autograd.grad(m(x), [x, *m.parameters()], gy)  # noqa: E731
+    g, out = _captured(step)
+    for rep in range(4):
+        with torch.no_grad():
+            x.copy_(torch.randn_like(x))
+        m.batch.docs.copy_(torch.tensor([0, 70 - rep, 71, 129], dtype=torch.int32))
+        g.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), rep
+
+
+@torch.no_grad()
+def test_a_captured_decode_step_replays_like_the_eager_one():
+    ms = [_layer(hidden=256) for _ in range(2)]
+    pages = torch.tensor([[5, 0, 7], [2, 6, 1], [3, 8, 4]], dtype=torch.int32, device="cuda")
+    text = torch.randn(40, 3, 256, device="cuda")
+    for m in ms:
+        m.new_cache(9, 16)
+    batch = CacheBatch.step(pages, [0, 0, 0], [1, 1, 1], 16)
+    h = text[0].clone()
+
+    def eager(t):
+        ms[1].batch = CacheBatch.step(pages, [t] * 3, [1] * 3, 16)
+        return ms[1](text[t])
+
+    ms[0].batch = batch
+    g, out = _captured(lambda: ms[0](h))
+    for t in range(40):
+        new = CacheBatch.step(pages, [t] * 3, [1] * 3, 16)
+        h.copy_(text[t])
+        for n in ("positions", "slots", "kv_lens"):
+            getattr(batch, n).copy_(getattr(new, n))
+        g.replay()
+        assert torch.equal(out, eager(t)), t
+    assert torch.equal(ms[0].k_cache, ms[1].k_cache) and torch.equal(ms[0].v_cache, ms[1].v_cache)
