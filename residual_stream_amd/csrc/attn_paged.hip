@@ -378,29 +378,25 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
 
 // Joins the splits' partial rows: Dh/4 lanes a row of [sequence][c][head], four
 // elements each, with a running maximum over the splits, eight of them in
-// flight at a time.
-template <int IO, int DH>
+// flight at a time.  Many splits (few rows, a chain of loads each) go to GROUPS
+// sets of lanes, which join what they found in LDS.
+constexpr int kJoinGroups = 8;
+template <int IO, int DH, int GROUPS>
 __global__ __launch_bounds__(kThreads) void attn_paged_join_kernel(PagedArgs a) {
-  constexpr int kLanes = DH / 4;
-  const int64_t n = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int e = threadIdx.x % kLanes * 4;
+  constexpr int kLanes = DH / 4, kPerRow = kLanes * GROUPS;
+  __shared__ float found[GROUPS > 1 ? 6 * kThreads : 1];
+  const int64_t n = (int64_t)blockIdx.x * (kThreads / kPerRow) + threadIdx.x / kPerRow;
+  const int e = threadIdx.x % kLanes * 4, group = threadIdx.x % kPerRow / kLanes;
   const int64_t sc = n / a.Hq;
   const int s = (int)(sc / a.max_q), c = (int)(sc % a.max_q), hq = (int)(n % a.Hq);
-  if (s >= a.n) return;
-  const Seq q = seq_of(a, s);
-  if (c >= q.nq) return;
+  Seq q{};
+  if (s < a.n) q = seq_of(a, s);
+  const bool real = s < a.n && c < q.nq;
+  if (GROUPS == 1 && !real) return;
   const int64_t row = (q.t0 + c) * a.Hq + hq, all = a.T * a.Hq;
   float m = -__builtin_inff(), total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
   constexpr int kAhead = 8;
-  for (int i = 0; i < a.splits; i += kAhead) {
-    float l[kAhead];
-    float4 v[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int64_t at = min(i + j, a.splits - 1) * all + row;
-      l[j] = i + j < a.splits ? a.part_l[at] : -__builtin_inff();
-      v[j] = *reinterpret_cast<const float4*>(a.part_o + at * DH + e);
-    }
+  auto take = [&](const float (&l)[kAhead], const float4 (&v)[kAhead]) {
     float top = m;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) top = fmaxf(top, l[j]);
@@ -418,6 +414,46 @@ __global__ __launch_bounds__(kThreads) void attn_paged_join_kernel(PagedArgs a) 
       acc[2] = __builtin_fmaf(w, v[j].z, acc[2]);
       acc[3] = __builtin_fmaf(w, v[j].w, acc[3]);
     }
+  };
+  if (real)
+    for (int i = group; i < a.splits; i += kAhead * GROUPS) {
+      float l[kAhead];
+      float4 v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int sp = i + j * GROUPS;
+        const int64_t at = min(sp, a.splits - 1) * all + row;
+        l[j] = sp < a.splits ? a.part_l[at] : -__builtin_inff();
+        v[j] = *reinterpret_cast<const float4*>(a.part_o + at * DH + e);
+      }
+      take(l, v);
+    }
+  if constexpr (GROUPS > 1) {
+    static_assert(GROUPS == kAhead, "one batch");
+    const float mine[6] = {m, total, acc[0], acc[1], acc[2], acc[3]};
+#pragma unroll
+    for (int k = 0; k < 6; ++k) found[k * kThreads + threadIdx.x] = mine[k];
+    __syncthreads();
+    if (!real || group != 0) return;
+    float sum = 0.f;
+    float l[kAhead];
+    float4 v[kAhead];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) {
+      const int at = threadIdx.x + j * kLanes;
+      l[j] = found[at];
+      v[j] = make_float4(found[2 * kThreads + at], found[3 * kThreads + at], found[4 * kThreads + at], found[5 * kThreads + at]);
+      top = fmaxf(top, l[j]);
+    }
+    const float base = top == -__builtin_inff() ? 0.f : top;
+#pragma unroll
+    for (int j = 0; j < GROUPS; ++j) sum = __builtin_fmaf(exp2_fast(l[j] - base), found[kThreads + threadIdx.x + j * kLanes], sum);
+    m = -__builtin_inff();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = 0.f;
+    take(l, v);
+    total = sum;
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
   const int64_t at = (q.t0 + c) * a.ldo + (int64_t)hq * DH + e;
@@ -506,7 +542,11 @@ hipError_t launch_attn_paged(const mhc_paged_desc& d, const void* q, const void*
     err = hipGetLastError();
     if (err != hipSuccess || a.splits == 1) return;
     const int64_t rows = (int64_t)d.n_seqs * d.max_q * d.Hq;
-    MHC_LAUNCH((attn_paged_join_kernel<IO, DH>), dim3((unsigned)((rows * (DH / 4) + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a);
+    auto blocks = [&](int lanes) { return dim3((unsigned)((rows * lanes + kThreads - 1) / kThreads)); };
+    if (a.splits > kJoinGroups)
+      MHC_LAUNCH((attn_paged_join_kernel<IO, DH, kJoinGroups>), blocks(DH / 4 * kJoinGroups), dim3(kThreads), 0, s, a);
+    else
+      MHC_LAUNCH((attn_paged_join_kernel<IO, DH, 1>), blocks(DH / 4), dim3(kThreads), 0, s, a);
     err = hipGetLastError();
   });
   return err;
