@@ -10,6 +10,14 @@
 // other), one over keys (dk, dv).  The scores are formed in both, seven
 // products instead of five.  P and dS are rounded to the I/O type for the
 // matrix cores; sums, δ and lse are fp32.
+//
+// Measured, bf16, causal, 40 query heads on 8 key heads of 128: 8192 tokens 985
+// us over rows (1046 TFLOP/s of the masked half's three products) and 1425 us
+// over keys (964 TFLOP/s of its four); nine documents of 4096 tokens with
+// capped scores 131 and 141 us, 16 us more for the sum of the pieces; 16 heads
+// of 64, 4096 tokens 90 and 110 us.  The matrix cores are busy 53 % and 45 % of
+// the time, LDS reads 36 % and 43 %, without bank conflicts, at 1.8 to 1.9 GHz
+// under the power limit (a large library product: 68 % busy).
 #include "attn_core.h"
 #include "mhc_internal.h"
 
@@ -221,7 +229,8 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
 
 // The same for grids that would not fill the chip: 32 rows a workgroup, held by
 // all four waves, which take the key tiles of 32 in turn, each through LDS of
-// its own, and add up their sums at the end.
+// its own, and add up their sums at the end (fp32, 777 tokens, 8 query heads on
+// 2 key heads of 64: 27 us instead of 73).
 template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_short_kernel(BwdArgs a) {
   using T = Tile<IO, DH>;
@@ -571,7 +580,9 @@ static bool tall_tiles(const mhc_attn_desc& d) {
   return d.io == MHC_BF16 && (d.Dh > 64 || d.T / (d.docs != nullptr ? d.n_docs : 1) >= 2048);
 }
 
-// Pieces of a key tile's steps: enough workgroups for two on every CU.
+// Pieces of a key tile's steps: enough workgroups for two on every CU (fp32,
+// 777 tokens, 8 query heads on 2 key heads of 64: 35 + 9 us for the sum instead
+// of 366; bound by the latency of a workgroup's few steps).
 static int pieces_of(const mhc_attn_desc& d) {
   const int64_t base = (d.T + kKeyRows - 1) / kKeyRows * d.Hk;
   int64_t n = (2 * device_cu_count() + base - 1) / base;

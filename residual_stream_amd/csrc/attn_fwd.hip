@@ -11,7 +11,19 @@
 //
 // A workgroup takes 128 rows of one query head, 32 a wave, and walks the keys
 // in tiles of 64, staged through registers into two LDS buffers (one barrier a
-// tile).  One pass, with a running maximum and sum per row.
+// tile).  One pass, with a running maximum and sum per row.  A wave's 32 rows
+// hold 64 accumulator and 32 query registers at heads of 128: two waves share
+// a SIMD, and one's softmax runs under the other's products.
+//
+// Measured, bf16, causal, 40 query heads on 8 key heads of 128: 8192 tokens
+// 740 us, 930 TFLOP/s of the products that the mask leaves (a large library
+// product reaches 1269); 4096 tokens 209 us; nine documents of 4096 tokens
+// with capped scores 98 us; 16 heads of 64, 4096 tokens 71 us.  The matrix
+// cores are busy 47 % of the time and the vector units about as long (half of
+// it the exponentials, at a quarter of the rate), LDS reads 36 %, without bank
+// conflicts; power holds the clock at 1.9 GHz.  A version whose eight waves
+// took products and softmax strictly in turns needed 12 % fewer cycles and 2 %
+// less time here, 5 to 15 % more time on the shorter cases.
 #include "attn_core.h"
 #include "mhc_internal.h"
 
@@ -131,7 +143,9 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_kernel
 
 // The same for grids that would not fill the chip: 32 rows a workgroup, held by
 // all four waves, which take the key tiles of 32 in turn, each through LDS of
-// its own (no barrier in the loop), and join their row states at the end.
+// its own (no barrier in the loop), and join their row states at the end
+// (fp32, 777 tokens, 8 query heads on 2 key heads of 64: 21 us instead of 53;
+// bound by the latency of a workgroup's few steps).
 template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_short_kernel(FwdArgs a) {
   using T = Tile<IO, DH>;
@@ -201,6 +215,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_short_
 
 }  // namespace
 
+// Fewer workgroups of 128 rows than CUs.
 bool attn_short(const mhc_attn_desc& d) { return (d.T + kRows - 1) / kRows * d.Hq < device_cu_count(); }
 
 attn::DocMask doc_mask(const mhc_attn_desc& d) {

@@ -17,6 +17,12 @@
 // as a fraction of a turn (p·f can be 10⁶ radians, where fp32 keeps no phase),
 // once per token in LDS for all its heads.  Everything in between is fp32;
 // each output is rounded once.
+//
+// Bound by HBM.  Measured, bf16, 4096 tokens of 40 and 8 heads of 128: forward
+// 20 us, 101 MB at 5.0 TB/s (a plain copy reaches 5.2); backward 38 us, 151 MB
+// at 4.0 TB/s (two row sums and the weights' products between a row's loads and
+// its stores; with loads rolled one row ahead it took 42 us), and 8
+// us to sum the weights' gradients.
 #include "mhc_device.h"
 #include "mhc_internal.h"
 
@@ -245,7 +251,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_rope_bwd_kernel(RopeArgs a) {
 }
 
 // Sum of the workgroups' partial rows: 16 columns a workgroup, 64 row slices
-// (at T = 4096, 2048 partial rows: 6 us, where 16 slices took 42).
+// (at T = 4096, 2048 partial rows: 8 us, where 16 slices took 42).
 __global__ __launch_bounds__(1024) void qk_rope_dw_kernel(const float* __restrict__ part, int rows, int Dh,
                                                           float* __restrict__ dqw, float* __restrict__ dkw) {
   __shared__ float red[1024];
