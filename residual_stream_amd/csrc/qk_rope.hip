@@ -19,10 +19,10 @@
 // each output is rounded once.
 //
 // Bound by HBM.  Measured, bf16, 4096 tokens of 40 and 8 heads of 128: forward
-// 20 us, 101 MB at 5.0 TB/s (a plain copy reaches 5.2); backward 38 us, 151 MB
-// at 4.0 TB/s (two row sums and the weights' products between a row's loads and
-// its stores; with loads rolled one row ahead it took 42 us), and 8
-// us to sum the weights' gradients.
+// 20 us, 101 MB at 5.0 TB/s (a plain copy reaches 5.2); backward 35 us, 151 MB
+// at 4.3 TB/s (two row sums and the weights' products between a row's loads and
+// its stores; loads rolled one row ahead made it 4 us slower), and 6 us to sum
+// the weights' gradients.
 #include "mhc_device.h"
 #include "mhc_internal.h"
 
@@ -166,13 +166,13 @@ __global__ __launch_bounds__(kRopeThreads) void qk_rope_kernel(RopeArgs a, int t
   }
 }
 
-// Backward.  Workgroups walk the tokens with the grid's stride, one token at a
+// Backward.  Workgroups walk the tokens with the grid's stride, one or two at a
 // time; each lane keeps the weight gradients of its 16 elements of q and of k
 // over all its rows, summed over the lane groups at the end into one partial
 // row per workgroup (fixed order, no atomics).
-template <int IO, int L>
+template <int IO, int L, int TOKENS>
 __global__ __launch_bounds__(kRopeThreads) void qk_rope_bwd_kernel(RopeArgs a) {
-  __shared__ float2 cs[kMaxHalfR];
+  __shared__ float2 cs[TOKENS * kMaxHalfR];
   __shared__ float red[kRopeThreads * 16];
   const int u = threadIdx.x % L;
   const bool live = u < a.Dh / 16;
@@ -182,11 +182,14 @@ __global__ __launch_bounds__(kRopeThreads) void qk_rope_bwd_kernel(RopeArgs a) {
   float dwq[16], dwk[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) dwq[j] = dwk[j] = 0.f;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    __syncthreads();  // the last token's angles have been read
-    angles(a, t, 1, cs);
+  for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.T; t0 += (int64_t)gridDim.x * TOKENS) {
+    const int nt = TOKENS > 1 && a.T - t0 > 1 ? 2 : 1;
+    __syncthreads();  // the last tokens' angles have been read
+    angles(a, t0, nt, cs);
     __syncthreads();
-    for (int head = threadIdx.x / L; head < heads; head += kRopeThreads / L) {
+    for (int n = threadIdx.x / L; n < nt * heads; n += kRopeThreads / L) {
+      const int tt = TOKENS > 1 && n >= heads ? 1 : 0, head = n - tt * heads;
+      const int64_t t = t0 + tt;
       const bool isq = head < a.Hq;
       const int hh = isq ? head : head - a.Hq;
       const int64_t so = t * (isq ? a.ldq : a.ldk) + (int64_t)hh * a.Dh;
@@ -205,7 +208,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_rope_bwd_kernel(RopeArgs a) {
           load8<kF32>(w, c1, wv + 8);
         }
       }
-      turn(a, cs, u, -1.f, g);
+      turn(a, cs + tt * (a.R / 2), u, -1.f, g);
       float ss = 0.f, sg = 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
@@ -251,7 +254,7 @@ __global__ __launch_bounds__(kRopeThreads) void qk_rope_bwd_kernel(RopeArgs a) {
 }
 
 // Sum of the workgroups' partial rows: 16 columns a workgroup, 64 row slices
-// (at T = 4096, 2048 partial rows: 8 us, where 16 slices took 42).
+// (at 2048 partial rows 8 us, where 16 slices took 42; at 1024 6).
 __global__ __launch_bounds__(1024) void qk_rope_dw_kernel(const float* __restrict__ part, int rows, int Dh,
                                                           float* __restrict__ dqw, float* __restrict__ dkw) {
   __shared__ float red[1024];
@@ -300,7 +303,12 @@ RopeArgs args_of(const mhc_rope_desc& d) {
   return a;
 }
 
-int bwd_workgroups(const mhc_rope_desc& d) { return (int)(d.T < 2048 ? d.T : 2048); }
+// Two tokens a workgroup at a time where there are enough of them: at T = 4096
+// the forward takes 19.7 instead of 20.6 us and the backward 35 instead of 38
+// (48 heads leave half of 32 lane groups idle every other round, 96 none); at
+// T = 8 the forward would take 8.9 instead of 6.6.
+int tokens_of(const mhc_rope_desc& d) { return d.T >= 4096 ? kRopeTokens : 1; }
+int bwd_workgroups(const mhc_rope_desc& d) { return (int)(d.T < 1024 ? d.T : 1024); }
 
 }  // namespace
 
@@ -320,9 +328,7 @@ hipError_t launch_qk_rope(const mhc_rope_desc& d, const void* q, const void* k, 
   a.vo = vo;
   a.slots = slots;
   a.n_slots = n_slots;
-  // two tokens a workgroup where there are enough of them (T = 4096: 19.6
-  // instead of 20.6 us; T = 8: 8.9 instead of 6.6)
-  const int tokens = d.T >= 4096 ? kRopeTokens : 1;
+  const int tokens = tokens_of(d);
   const dim3 grid((unsigned)((d.T + tokens - 1) / tokens));
   dispatch_io(d.io, [&](auto io_) {
     dispatch_lanes(d.Dh, [&](auto l_) {
@@ -362,7 +368,10 @@ hipError_t launch_qk_rope_bwd(const mhc_rope_desc& d, const void* dqo, const voi
     dispatch_lanes(d.Dh, [&](auto l_) {
       constexpr int IO = decltype(io_)::value;
       constexpr int L = decltype(l_)::value;
-      MHC_LAUNCH((qk_rope_bwd_kernel<IO, L>), dim3((unsigned)nwg), dim3(kRopeThreads), 0, s, a);
+      if (tokens_of(d) > 1)
+        MHC_LAUNCH((qk_rope_bwd_kernel<IO, L, 2>), dim3((unsigned)nwg), dim3(kRopeThreads), 0, s, a);
+      else
+        MHC_LAUNCH((qk_rope_bwd_kernel<IO, L, 1>), dim3((unsigned)nwg), dim3(kRopeThreads), 0, s, a);
     });
   });
   if (weights) MHC_LAUNCH(qk_rope_dw_kernel, dim3((unsigned)(2 * d.Dh / 16)), dim3(1024), 0, s, a.part, nwg, d.Dh, dqw, dkw);
