@@ -33,7 +33,7 @@ def _bound(y, big, io):
 SHAPES = [(1, 1, 1, 16, 16), (3, 5, 1, 32, 16), (70, 8, 2, 64, 64), (33, 6, 3, 96, 48), (129, 40, 8, 128, 128),
           (5, 3, 3, 128, 112), (9, 4, 2, 256, 64), (2, 2, 1, 512, 512), (17, 3, 1, 208, 160),
           # two tokens a workgroup at a time (the weights' sums are chains of 61 additions at most)
-          (4096, 3, 1, 128, 128), (4097, 5, 2, 128, 64)]
+          (4096, 3, 1, 128, 128), (4097, 6, 2, 128, 64)]
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
