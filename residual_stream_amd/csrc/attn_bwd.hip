@@ -230,7 +230,8 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_k
 // The same for grids that would not fill the chip: 32 rows a workgroup, held by
 // all four waves, which take the key tiles of 32 in turn, each through LDS of
 // its own, and add up their sums at the end (fp32, 777 tokens, 8 query heads on
-// 2 key heads of 64: 27 us instead of 73).
+// 2 key heads of 64: 27 us instead of 73).  Not for bf16 heads of 128, where
+// the registers do not hold it (8 heads, 2048 tokens: 84 us instead of 72).
 template <int IO, int DH, int MOD>
 __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_bwd_rows_short_kernel(BwdArgs a) {
   using T = Tile<IO, DH>;
@@ -628,7 +629,7 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
   a.lddq = d.ld_dq;
   a.lddk = d.ld_dk;
   a.lddv = d.ld_dv;
-  const bool small = attn_short(d);
+  const bool small = attn_short(d) && (d.io == MHC_F32 || d.Dh == 64);
   const int per = small ? 32 : kRows;
   const dim3 rows((unsigned)((d.T + per - 1) / per * d.Hq));
   const bool tall = tall_tiles(d);
@@ -639,10 +640,10 @@ hipError_t launch_attn_bwd(const mhc_attn_desc& d, const void* dout, const void*
     constexpr int DH = decltype(dh_)::value;
     constexpr int MOD = decltype(mod_)::value;
     constexpr int row = Tile<IO, DH>::kRow;
-    constexpr int few = 8 * 32 * row > wave_states_bytes<DH>() ? 8 * 32 * row : wave_states_bytes<DH>();
-    if (small)
-      MHC_LAUNCH((attn_bwd_rows_short_kernel<IO, DH, MOD>), rows, dim3(kThreads), few, s, a);
-    else
+    [[maybe_unused]] constexpr int few = 8 * 32 * row > wave_states_bytes<DH>() ? 8 * 32 * row : wave_states_bytes<DH>();
+    if constexpr (IO == kF32 || DH == 64)
+      if (small) MHC_LAUNCH((attn_bwd_rows_short_kernel<IO, DH, MOD>), rows, dim3(kThreads), few, s, a);
+    if (!small)
       MHC_LAUNCH((attn_bwd_rows_kernel<IO, DH, MOD>), rows, dim3(kThreads), 4 * kKeys * row, s, a);
     err = hipGetLastError();
     if (err != hipSuccess) return;

@@ -215,8 +215,20 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_fwd_short_
 
 }  // namespace
 
-// Fewer workgroups of 128 rows than CUs.
-bool attn_short(const mhc_attn_desc& d) { return (d.T + kRows - 1) / kRows * d.Hq < device_cu_count(); }
+// Whether 128 rows a workgroup would leave the chip too empty: fewer workgroups
+// than CUs, or than two a CU where documents are long (so that a workgroup is a
+// long chain of steps) and the kernels of 32 rows hold their state in registers
+// with room to spare (not bf16 heads of 128).  Measured, 128 and 32 rows, the
+// forward and the backward's rows kernel, us: bf16, 16 heads of 64, 2309 rows
+// 46 + 55 and 34 + 44; the same in documents of 100 rows 16.5 + 19 and 16.4 +
+// 23; 4096 rows in 16 documents 17 + 23 and 24 + 35; fp32, 8 heads of 64, 4096
+// rows 296 + 418 and 167 + 253; bf16, 40 heads of 128, 1024 rows 36 + 51 and 41
+// + 82, but 8 heads of 128, 2048 rows 53 and 29 (forward).
+bool attn_short(const mhc_attn_desc& d) {
+  const bool roomy = d.io == MHC_F32 || d.Dh == 64;
+  const bool chains = d.T / (d.docs != nullptr ? d.n_docs : 1) >= 512;
+  return (d.T + kRows - 1) / kRows * d.Hq < (roomy && chains ? 2 : 1) * device_cu_count();
+}
 
 attn::DocMask doc_mask(const mhc_attn_desc& d) {
   attn::DocMask m;
