@@ -4,7 +4,10 @@ documents with its backward, and attention of new tokens over a paged cache.
 
 Argument marshalling only, in the manner of :mod:`residual_stream_amd.mhc`:
 every step runs in the gfx950 kernels of ``libmhc.so`` on torch's current
-stream, outputs and workspaces are torch's, and there is no CPU path.
+stream, outputs and workspaces are torch's, and there is no CPU path.  With
+``stream`` a call is made as within ``torch.cuda.stream(stream)``: it runs
+there, and the tensors it makes belong to that stream (the inputs must be ready
+on it).
 
 Head tensors are [T, H, Dh] in float32 or bfloat16 with contiguous heads and
 any token stride that is a multiple of 8 elements, so q, k and v may be views
@@ -108,8 +111,13 @@ def _like(t):
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
-def _stream_of(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _within(stream, call, args):
+    """``call`` as made within ``torch.cuda.stream(stream)``: its output and
+    workspace then come from that stream's memory, where nothing else can take
+    them while the kernels run."""
+    args["stream"] = None
+    with torch.cuda.stream(stream):
+        return call(**args)
 
 
 def _scratch(need, workspace, device):
@@ -119,7 +127,10 @@ def _scratch(need, workspace, device):
             return None, 0, None
         workspace = _workspace(need, device)
         return workspace.data_ptr(), need, workspace
-    return workspace.data_ptr(), _ws_bytes(workspace), workspace
+    nbytes = _ws_bytes(workspace)
+    if workspace.device != device:
+        raise ValueError(f"the workspace is on {workspace.device}, expected {device}")
+    return workspace.data_ptr(), nbytes, workspace
 
 
 def rope_freqs(rotated: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -151,6 +162,8 @@ def mhc_qk_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-
     positions[T] (int32) times freqs (float64, :func:`rope_freqs`).
 
     Returns (q_out[T,Hq,Dh], k_out[T,Hk,Dh])."""
+    if stream is not None:
+        return _within(stream, mhc_qk_rope, locals())
     lib = load()
     d, ks, at, dtype, dev = _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
     if out is None:
@@ -160,7 +173,7 @@ def mhc_qk_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-
         qo, ko = out
         d.ldq_out = _heads("q_out", qo, q.shape, dtype, dev)
         d.ldk_out = _heads("k_out", ko, ks, dtype, dev)
-    _check(lib.mhc_qk_rope(_ref(d), *at, qo.data_ptr(), ko.data_ptr(), _stream_of(stream, dev)), "mhc_qk_rope")
+    _check(lib.mhc_qk_rope(_ref(d), *at, qo.data_ptr(), ko.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)), "mhc_qk_rope")
     return out
 
 
@@ -169,6 +182,8 @@ def mhc_qk_rope_bwd(dq_out, dk_out, q, k, positions, freqs, *, q_weight=None, k_
     """Backward of :func:`mhc_qk_rope` from its inputs: returns (dq, dk,
     dq_weight[Dh] or None, dk_weight[Dh] or None), the weights' gradients in
     fp32 summed over tokens and heads."""
+    if stream is not None:
+        return _within(stream, mhc_qk_rope_bwd, locals())
     lib = load()
     d, ks, at, dtype, dev = _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
     d.ldq_out = _heads("dq_out", dq_out, q.shape, dtype, dev)
@@ -187,7 +202,7 @@ def mhc_qk_rope_bwd(dq_out, dk_out, q, k, positions, freqs, *, q_weight=None, k_
         grads = (_vec("dq_weight", dqw, row, torch.float32, dev), _vec("dk_weight", dkw, row, torch.float32, dev))
     ws, nbytes, _keep = _scratch(lib.mhc_qk_rope_bwd_workspace_bytes(_ref(d)), workspace, q.device)
     _check(lib.mhc_qk_rope_bwd(_ref(d), dq_out.data_ptr(), dk_out.data_ptr(), *at, dq.data_ptr(), dk.data_ptr(), *grads,
-                               ws, nbytes, _stream_of(stream, dev)), "mhc_qk_rope_bwd")
+                               ws, nbytes, torch._C._cuda_getCurrentRawStream(dev)), "mhc_qk_rope_bwd")
     return out
 
 
@@ -207,6 +222,8 @@ def mhc_qk_rope_cache(q, k, v, positions, freqs, k_cache, v_cache, slots, *, q_w
     of the caches [pages, page_size, Hk, Dh]; a slot outside them (-1 for a
     padded token) writes nothing.  Slots of one call must differ.  Returns
     q_out[T,Hq,Dh]."""
+    if stream is not None:
+        return _within(stream, mhc_qk_rope_cache, locals())
     lib = load()
     d, ks, at, dtype, dev = _rope(q, k, positions, freqs, q_weight, k_weight, eps, interleaved)
     d.ldv = _heads("v", v, ks, dtype, dev)
@@ -217,7 +234,7 @@ def mhc_qk_rope_cache(q, k, v, positions, freqs, k_cache, v_cache, slots, *, q_w
     else:
         d.ldq_out = _heads("q_out", out, q.shape, dtype, dev)
     _check(lib.mhc_qk_rope_cache(_ref(d), at[0], at[1], v.data_ptr(), *at[2:], out.data_ptr(), kc, vc, to, pages * size,
-                                 _stream_of(stream, dev)), "mhc_qk_rope_cache")
+                                 torch._C._cuda_getCurrentRawStream(dev)), "mhc_qk_rope_cache")
     return out
 
 
@@ -275,6 +292,8 @@ def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=
     log-sum-exps [Hq, T].  Rows of no document come out as zeros (lse -inf); in
     tensors passed as ``out=(o, saved or None)`` they are left as they were,
     unless fill_outside is true."""
+    if stream is not None:
+        return _within(stream, mhc_attn, locals())
     lib = load()
     d, _ks, at, dtype, dev = _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
     d.fill_outside = 1 if (out is None if fill_outside is None else fill_outside) else 0
@@ -285,7 +304,7 @@ def mhc_attn(q, k, v, *, docs=None, causal=True, prefix=None, window=0, softcap=
         o, saved = out
         d.ldo = _heads("o", o, q.shape, dtype, dev)
     lse, rest = (None, None) if saved is None else _saved(saved, d, dev)
-    _check(lib.mhc_attn(_ref(d), *at, o.data_ptr(), lse, rest, _stream_of(stream, dev)), "mhc_attn")
+    _check(lib.mhc_attn(_ref(d), *at, o.data_ptr(), lse, rest, torch._C._cuda_getCurrentRawStream(dev)), "mhc_attn")
     return out
 
 
@@ -295,6 +314,8 @@ def mhc_attn_bwd(do, q, k, v, o, saved, *, docs=None, causal=True, prefix=None, 
     dv), dk and dv summed over the query heads that share a key head.  Rows of
     no document get zeros; in tensors passed as ``out`` they are left as they
     were, unless fill_outside is true."""
+    if stream is not None:
+        return _within(stream, mhc_attn_bwd, locals())
     lib = load()
     d, ks, at, dtype, dev = _attn(q, k, v, docs, causal, prefix, window, softcap, slopes, scale)
     d.ld_do = _heads("do", do, q.shape, dtype, dev)
@@ -311,7 +332,7 @@ def mhc_attn_bwd(do, q, k, v, o, saved, *, docs=None, causal=True, prefix=None, 
         d.ld_dv = _heads("dv", dv, ks, dtype, dev)
     ws, nbytes, _keep = _scratch(lib.mhc_attn_bwd_workspace_bytes(_ref(d)), workspace, q.device)
     _check(lib.mhc_attn_bwd(_ref(d), do.data_ptr(), *at, o.data_ptr(), lse, rest, dq.data_ptr(), dk.data_ptr(),
-                            dv.data_ptr(), ws, nbytes, _stream_of(stream, dev)), "mhc_attn_bwd")
+                            dv.data_ptr(), ws, nbytes, torch._C._cuda_getCurrentRawStream(dev)), "mhc_attn_bwd")
     return out
 
 
@@ -330,6 +351,8 @@ def mhc_attn_paged(q, k_cache, v_cache, pages, kv_lens, *, cu_q=None, max_q=None
     Returns o[T,Hq,Dh]; a row without a key gets zeros, a row whose keys lie in
     a page outside the cache NaN; rows of no sequence get zeros, or are left as
     they were in a tensor passed as ``out``."""
+    if stream is not None:
+        return _within(stream, mhc_attn_paged, locals())
     lib = load()
     shape, dtype, io, dev = _queries(q)
     T, Hq, Dh = shape
@@ -360,6 +383,6 @@ def mhc_attn_paged(q, k_cache, v_cache, pages, kv_lens, *, cu_q=None, max_q=None
     else:
         d.ldo = _heads("o", out, shape, dtype, dev)
     ws, nbytes, _keep = _scratch(lib.mhc_attn_paged_workspace_bytes(_ref(d)), workspace, q.device)
-    _check(lib.mhc_attn_paged(_ref(d), q.data_ptr(), kc, vc, out.data_ptr(), ws, nbytes, _stream_of(stream, dev)),
+    _check(lib.mhc_attn_paged(_ref(d), q.data_ptr(), kc, vc, out.data_ptr(), ws, nbytes, torch._C._cuda_getCurrentRawStream(dev)),
            "mhc_attn_paged")
     return out

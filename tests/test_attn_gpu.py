@@ -285,3 +285,30 @@ def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(io, Dh, Hq
     close("o", np.where(hit, ro, o), ro, eo)
     only = ok[:, 60] & ~ok[:, 130]
     assert (o[only][:, :, 3] == inf).all()
+
+
+def test_another_stream_than_the_current_one():
+    """Outputs and workspaces of a call on `stream` are that stream's: memory the current one takes meanwhile is not theirs."""
+    (q, k, v, do), kw, *_ = _case("bf16", 700, 8, 2, 128, seed=3, docs=[0, 300, 700])
+    want = attn.mhc_attn(q, k, v, **kw)
+    grads = attn.mhc_attn_bwd(do, q, k, v, *want, **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for rep in range(5):
+        got = attn.mhc_attn(q, k, v, stream=side, **kw)
+        back = attn.mhc_attn_bwd(do, q, k, v, *got, stream=side, **kw)
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 18, 1 << 20, 1 << 22) for _ in range(4)]
+        torch.cuda.synchronize()
+        for n, a, b in zip(("o", "saved", "dq", "dk", "dv"), (*got, *back), (*want, *grads)):
+            same(f"{n} {rep}", a, b)
+        del junk
+
+
+def test_workspaces_that_are_refused():
+    (q, k, v, do), kw, *_ = _case("f32", 40, 2, 2, 64, seed=4)
+    o, saved = attn.mhc_attn(q, k, v, **kw)
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            attn.mhc_attn_bwd(do, q, k, v, o, saved, workspace=ws, **kw)
+    with pytest.raises(mhc.MhcError):
+        attn.mhc_attn_bwd(do, q, k, v, o, saved, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), **kw)
