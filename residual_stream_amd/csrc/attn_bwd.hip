@@ -583,7 +583,11 @@ static bool tall_tiles(const mhc_attn_desc& d) {
 
 // Pieces of a key tile's steps: enough workgroups for two on every CU (fp32,
 // 777 tokens, 8 query heads on 2 key heads of 64: 35 + 9 us for the sum instead
-// of 366; bound by the latency of a workgroup's few steps).
+// of 366; bound by the latency of a workgroup's few steps).  Enough for one and
+// for four: 4096 rows in nine uneven documents, 40 heads on 8 of 128, 266 and
+// 150 + 25 us instead of 149 + 16; 2048 rows, the same heads, 164 + 10 and 128
+// + 24 instead of 109 + 15 (sixteen equal documents of 256 rows would take 53
+// instead of 65 + 16 with one, but lengths are not known here).
 static int pieces_of(const mhc_attn_desc& d) {
   const int64_t base = (d.T + kKeyRows - 1) / kKeyRows * d.Hk;
   int64_t n = (2 * device_cu_count() + base - 1) / base;
