@@ -343,8 +343,8 @@ class CacheBatch:
         dev = pages.device
         if any(n > 0 and -(-(d + n) // page_size) > pages.shape[1] for d, n in zip(done, new)):
             raise ValueError("a sequence outgrows its page table")
-        seq = torch.tensor([s for s, n in enumerate(new) for _ in range(n)], device=dev)
-        pos = torch.tensor([p for d, n in zip(done, new) for p in range(d, d + n)], device=dev)
+        seq = torch.tensor([s for s, n in enumerate(new) for _ in range(n)], dtype=torch.int64, device=dev)
+        pos = torch.tensor([p for d, n in zip(done, new) for p in range(d, d + n)], dtype=torch.int64, device=dev)
         slots = pages[seq, pos // page_size].long() * page_size + pos % page_size
         ints = lambda a: torch.tensor(list(a), dtype=torch.int32, device=dev)  # noqa: E731
         one = all(n == 1 for n in new)

@@ -233,3 +233,19 @@ def test_a_captured_decode_step_replays_like_the_eager_one():
         g.replay()
         assert torch.equal(out, eager(t)), t
     assert torch.equal(ms[0].k_cache, ms[1].k_cache) and torch.equal(ms[0].v_cache, ms[1].v_cache)
+
+
+def test_no_tokens():
+    m = _layer()
+    m.batch = AttnBatch(torch.zeros(0, dtype=torch.int32, device="cuda"))
+    x = torch.zeros((0, 128), device="cuda", requires_grad=True)
+    y = m(x)
+    y.sum().backward()
+    assert y.shape == x.grad.shape == (0, 128)
+    assert all(int(torch.count_nonzero(p.grad)) == 0 for p in m.parameters())
+    m.new_cache(4, 16)
+    pages = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    with torch.no_grad():
+        m.batch = CacheBatch.step(pages, [3, 0], [0, 0], 16)
+        assert m(x.detach()).shape == (0, 128)
+    assert int(torch.count_nonzero(m.k_cache)) == 0
