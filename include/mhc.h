@@ -374,7 +374,8 @@ mhc_status mhc_attn_bwd(const mhc_attn_desc* desc, const void* dout, const void*
 /* Attention of new tokens over a paged cache [num_pages][page_size][Hk][Dh].
  * The rows of q and o are packed by sequence: sequence s has rows
  * cu_q[s] .. cu_q[s+1] - 1 (device, int32[n_seqs + 1], sorted; NULL: row s
- * alone), at most max_q of them (further rows are not computed).  kv_lens[s]
+ * alone), at most max_q of them (further rows count as rows of no sequence,
+ * but as positions of theirs).  kv_lens[s]
  * (device, int32) counts its keys, the new tokens' included: the cache already
  * holds those.  Key j lies in page pages[s][j / page_size] (device,
  * int32[n_seqs][max_pages]) at offset j mod page_size; entries past the last

@@ -345,8 +345,9 @@ def mhc_attn_paged(q, k_cache, v_cache, pages, kv_lens, *, cu_q=None, max_q=None
     (int32) its keys with the new ones.  Without cu_q, row s of q[T,Hq,Dh] is
     sequence s's next token; with cu_q (int32 [n+1], sorted) rows cu_q[s] ..
     cu_q[s+1]-1 are its last tokens, at most max_q of them (a host number; T if
-    None: give the longest chunk, the grid is sized by it).  Masks and scores as
-    :func:`mhc_attn`, positions counted within each sequence.
+    None: give the longest chunk, the grid is sized by it; a sequence's rows past
+    max_q count as rows of no sequence).  Masks and scores as :func:`mhc_attn`,
+    positions counted within each sequence.
 
     Returns o[T,Hq,Dh]; a row without a key gets zeros, a row whose keys lie in
     a page outside the cache NaN; rows of no sequence get zeros, or are left as

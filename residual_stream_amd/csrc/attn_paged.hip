@@ -71,24 +71,23 @@ struct PagedArgs {
 // Sequence `s`: its first row, number of rows and number of keys, all within
 // the tensors whatever the device arrays hold.
 struct Seq {
-  int64_t t0;
+  int64_t t0, t1;  // rows, of which the first nq are computed
   int nq, nk;
   int before;  // keys before the first new token's own (negative: rows without keys)
 };
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 __device__ __forceinline__ Seq seq_of(const PagedArgs& a, int s) {
   Seq q;
-  int64_t t1;
   if (a.cu == nullptr) {
     q.t0 = s;
-    t1 = s + 1;
+    q.t1 = s + 1;
   } else {
     q.t0 = clamp64(a.cu[s], 0, a.T);
-    t1 = clamp64(a.cu[s + 1], q.t0, a.T);
+    q.t1 = clamp64(a.cu[s + 1], q.t0, a.T);
   }
-  q.nq = (int)(t1 - q.t0 < a.max_q ? t1 - q.t0 : a.max_q);
+  q.nq = (int)(q.t1 - q.t0 < a.max_q ? q.t1 - q.t0 : a.max_q);
   q.nk = (int)clamp64(a.kv[s], 0, (int64_t)a.max_pages * a.page_size);
-  q.before = (int)clamp64(q.nk - (t1 - q.t0), -(int64_t)0x7fffffff, q.nk);
+  q.before = (int)clamp64(q.nk - (q.t1 - q.t0), -(int64_t)0x7fffffff, q.nk);
   return q;
 }
 
@@ -191,6 +190,16 @@ __device__ __forceinline__ void fill_rest(const PagedArgs& a) {
   }
 }
 
+// A sequence's rows past max_q likewise, for the heads of key head hk.
+template <int IO, int DH>
+__device__ __forceinline__ void fill_past(const PagedArgs& a, const Seq& q, int hk) {
+  if (!a.fill) return;
+  const int G = a.Hq / a.Hk;
+  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t t = q.t0 + q.nq; t < q.t1; ++t)
+    for (int e = threadIdx.x * 8; e < G * DH; e += blockDim.x * 8) store8<IO>(a.o, t * a.ldo + (int64_t)hk * G * DH + e, z);
+}
+
 // Writes a finished row (or a split's share of it).
 template <int IO, int DH>
 __device__ __forceinline__ void finish(const PagedArgs& a, const Row& r, int sp, int h, RowState<DH>& st, float l, bool bad) {
@@ -241,6 +250,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_few_
   const int rest = blockIdx.x / a.Hk, sp = rest % a.splits, s = rest / a.splits;
   const Seq q = seq_of(a, s);
   if (q.nq == 0) return;
+  if (sp == 0) fill_past<IO, DH>(a, q, hk);
   const Row r = row_of(a, s, q, hk, c);
   int lo, hi;
   wave_range(r.lo, r.hi, lo, hi);
@@ -319,6 +329,7 @@ __global__ __launch_bounds__(kThreads, IO == kBF16 ? 2 : 1) void attn_paged_chun
   const int G = a.Hq / a.Hk;
   const Seq q = seq_of(a, s);
   if ((int64_t)tile * kRows >= (int64_t)q.nq * G) return;
+  if (sp == 0 && tile == 0) fill_past<IO, DH>(a, q, hk);
   const Row r = row_of(a, s, q, hk, tile * kRows + wave * 32 + c);
   int wlo, whi;
   wave_range(r.lo, r.hi, wlo, whi);

@@ -251,3 +251,23 @@ def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(io, new, H
     hit = np.broadcast_to(hit[:, None], o.shape)
     assert not np.isfinite(o[hit]).any()
     close("o", np.where(hit, ref, o), ref, bound + 2.0 ** -20 * np.abs(ref).max())
+
+
+@pytest.mark.parametrize("new,max_q", [(9, 4), (100, 70)])
+def test_rows_past_the_given_longest_chunk(new, max_q):
+    Hq, Hk, Dh, page = 8, 2, 64, 16
+    kv = [300, 170, 40]
+    lens = [new, 3, new]
+    q, kc, vc, table = _paged("f32", kv, lens, Hq, Hk, Dh, page, seed=8, poison=False)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    call = lambda **k: attn.mhc_attn_paged(q, kc, vc, table, ints(kv), cu_q=ints(cu), **k)  # noqa: E731
+    whole = call(max_q=new)
+    past = np.concatenate([np.arange(a + max_q, b) for a, b in zip(cu, cu[1:])])
+    rest = np.setdiff1d(np.arange(len(q)), past)
+    got = call(max_q=max_q)
+    assert int(torch.count_nonzero(got[past])) == 0
+    close("o", host(got)[rest], host(whole)[rest], 2.0 ** -18 * np.abs(host(whole)).max() * np.ones(1))
+    given = torch.full_like(q, 7.0)
+    call(max_q=max_q, out=given)
+    assert bool((given[past] == 7.0).all())
+    same("given", given[rest], got[rest])
